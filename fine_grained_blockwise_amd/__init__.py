@@ -24,7 +24,9 @@ __all__ = [
     "fp8_direct_transpose_fmt", "mx2_quant_rule", "fp8_block_gemm_fmt", "fp8_grouped_gemm_masked",
     "permute_pad_noalloc", "PERMUTE_PAD_NOALLOC_SCRATCH_BYTES", "fgb_hbm_probe",
     "PROBE_COPY", "PROBE_READ", "PROBE_FILL", "PROBE_STRIDED_READ", "PROBE_STRIDED_WRITE",
-    "E4M3", "E5M2", "SCALE_CEIL", "SCALE_OCP_FLOOR", "F32", "BF16", "ROW1x128", "ROW1x32", "BLOCK128", "GEMM_EXACT", "GEMM_FAST",
+    "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm", "mxfp4_grouped_gemm",
+    "moe_router", "moe_router_backward", "moe_router_workspace_size", "ROUTER_SOFTMAX", "ROUTER_SIGMOID",
+    "E4M3", "E5M2", "E2M1", "SCALE_CEIL", "SCALE_OCP_FLOOR", "F32", "BF16", "ROW1x128", "ROW1x32", "BLOCK128", "GEMM_EXACT", "GEMM_FAST",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,8 +35,9 @@ LIB_PATH = os.path.join(HERE, "libfgb.so")
 F32, BF16 = 0, 1
 ROW1x128, ROW1x32, BLOCK128 = 0, 1, 2
 GEMM_EXACT, GEMM_FAST = 0, 1
-E4M3, E5M2 = 0, 1
+E4M3, E5M2, E2M1 = 0, 1, 2
 SCALE_CEIL, SCALE_OCP_FLOOR = 0, 1
+ROUTER_SOFTMAX, ROUTER_SIGMOID = 0, 1
 PROBE_COPY, PROBE_READ, PROBE_FILL, PROBE_STRIDED_READ, PROBE_STRIDED_WRITE = 0, 1, 2, 3, 4
 
 SYMBOLS = [
@@ -46,7 +49,8 @@ SYMBOLS = [
     "fp8_grouped_direct_transpose", "fp8_kgrouped_gemm", "swiglu_quant_cache", "unpermute_backward_quant",
     "fp8_quant_rowwise_fmt", "fp8_dequant_fmt", "fgb_fp8_encode", "fp8_direct_transpose_fmt", "mx2_quant_rule",
     "fp8_block_gemm_fmt", "fp8_grouped_gemm_masked", "fp8_quant_blockwise_t", "swiglu_f32", "dswiglu_f32",
-    "permute_pad_noalloc", "fgb_hbm_probe",
+    "permute_pad_noalloc", "fgb_hbm_probe", "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm",
+    "mxfp4_grouped_gemm", "moe_router", "moe_router_workspace_size", "moe_router_backward",
 ]
 
 
@@ -61,7 +65,7 @@ if not os.path.exists(LIB_PATH):
                       "`python -c 'import __graft_entry__ as g; g.build()'`")
 
 _lib = C.CDLL(LIB_PATH)
-_p, _i64, _i32, _sz = C.c_void_p, C.c_int64, C.c_int, C.c_size_t
+_p, _i64, _i32, _sz, _f32 = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float
 _SIG = {
     "fgb_last_error": (C.c_char_p, []),
     "fgb_version": (C.c_char_p, []),
@@ -104,6 +108,15 @@ _SIG = {
     "mx2_dequant": (_i32, [_p, _p, _p, _i64, _i64, _i64, _p, _p]),
     "swiglu_f32": (_i32, [_p, _p, _i64, _p, _p]),
     "dswiglu_f32": (_i32, [_p, _p, _p, _i64, _p, _p, _p]),
+    "mxfp4_quant": (_i32, [_p, _i32, _i32, _i64, _i64, _i64, _i32, _p, _p, _p]),
+    "mxfp4_quant_t": (_i32, [_p, _i32, _i32, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p]),
+    "mxfp4_dequant": (_i32, [_p, _p, _i64, _i64, _p, _i32, _p]),
+    "mxfp4_gemm": (_i32, [_p, _p, _i32, _p, _p, _i64, _i64, _i64, _i64, _i64, _p, _i32, _i64, _i32, _p]),
+    "mxfp4_grouped_gemm": (_i32, [_p, _p, _i32, _p, _p, _p, _i32, _i64, _i64, _i64, _p, _i32, _p]),
+    "moe_router": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _i32, _i32, _f32, _f32, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_router_workspace_size": (_sz, [_i64, _i32]),
+    "moe_router_backward": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _p, _p, _p, _i32, _i32, _f32, _f32, _p, _i64,
+                                   _p]),
 }
 for _name, (_res, _args) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -880,3 +893,184 @@ def mx2_dequant(q, s2, s1, g1=10240):
     _call("mx2_dequant", _ptr(q.contiguous()), _ptr(s2.contiguous()), _ptr(s1.contiguous()), R, Cc,
           g1, _ptr(out), _stream(q))
     return out
+
+
+# ---------------------------------------------------------------------------
+def _mxfp4_shapes(rows, cols):
+    """Shapes of the codes and scales of an MXFP4 tensor of `rows` x `cols` values."""
+    return (rows, cols // 2), ((cols + 255) // 256, rows, 8)
+
+
+def _mxfp4_input(x, name):
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name}: x must be [rows, cols] or [G, rows, cols]")
+    _dtype_code(x)
+    rows, cols = x.shape[-2:]
+    if cols % 32:
+        raise ValueError(f"{name}: cols ({cols}) must be a multiple of 32")
+    _check_dev(x)
+    # anything but aligned rows of unit stride (stacked without gaps) is copied once
+    ld = x.stride(-2)
+    if (x.stride(-1) != 1 or ld < cols or ld * x.element_size() % 16 or x.data_ptr() % 16
+            or (x.dim() == 3 and x.stride(0) != rows * ld)):
+        x = x.contiguous() if not x.is_contiguous() else x.clone()
+    return x
+
+
+def _mxfp4_out(x, lead, rows, cols):
+    qs, ss = _mxfp4_shapes(rows, cols)
+    return [torch.empty(lead + shp, dtype=torch.uint8, device=x.device) for shp in (qs, ss)]
+
+
+def mxfp4_quant(x, rule=SCALE_CEIL):
+    """MXFP4 quantization of x [rows, cols] (fp32/bf16, cols % 32 == 0) -> (q uint8 [rows, cols/2],
+    s uint8 [ceil(cols/256), rows, 8]), or of stacked matrices x [G, rows, cols] -> (q [G, ...], s [G, ...]);
+    see include/fgb.h for the layouts."""
+    x = _mxfp4_input(x, "mxfp4_quant")
+    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
+    q, s = _mxfp4_out(x, lead, rows, cols)
+    _call("mxfp4_quant", _ptr(x), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule, _ptr(q),
+          _ptr(s), _stream(x))
+    return q, s
+
+
+def mxfp4_quant_t(x, rule=SCALE_CEIL):
+    """MXFP4 quantization of x [rows, cols] (or [G, rows, cols]) and of its transpose, in one pass:
+    -> (q, s, qt, st), qt and st being those of a [cols, R] tensor, R = rows rounded up to 32 (columns past rows
+    are zeros)."""
+    x = _mxfp4_input(x, "mxfp4_quant_t")
+    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
+    q, s = _mxfp4_out(x, lead, rows, cols)
+    qt, st = _mxfp4_out(x, lead, cols, (rows + 31) // 32 * 32)
+    _call("mxfp4_quant_t", _ptr(x), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule, _ptr(q),
+          _ptr(s), _ptr(qt), _ptr(st), _stream(x))
+    return q, s, qt, st
+
+
+def mxfp4_dequant(q, s, out_dtype=torch.float32):
+    """decode(q) * 2^(s-127) -> [rows, cols] (fp32 or bf16)."""
+    _check_2d_codes(q, "mxfp4_dequant: q")
+    rows, cols = q.shape[0], 2 * q.shape[1]
+    _need(s, "mxfp4_dequant: s", shape=_mxfp4_shapes(rows, cols)[1], dtype=torch.uint8, contiguous=True)
+    _need(q, "mxfp4_dequant: q", contiguous=True)
+    _out_dtype(out_dtype, "mxfp4_dequant")
+    _check_dev(q, s)
+    out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
+    _call("mxfp4_dequant", _ptr(q), _ptr(s), rows, cols, _ptr(out), _dtype_code(out), _stream(q))
+    return out
+
+
+def _mxfp4_a(a, sa, a_fmt, name):
+    """K of the A operand, its scales checked against it."""
+    _check_2d_codes(a, f"{name}: a")
+    if a_fmt not in (E2M1, E4M3):
+        raise ValueError(f"{name}: a_fmt must be E2M1 or E4M3")
+    M, K = a.shape[0], a.shape[1] * (2 if a_fmt == E2M1 else 1)
+    shape = _mxfp4_shapes(M, K)[1] if a_fmt == E2M1 else (M, K // 128)
+    _need(sa, f"{name}: sa", shape=shape, dtype=torch.uint8, contiguous=True)
+    return M, K
+
+
+def mxfp4_gemm(a, sa, b, sb, a_fmt=E2M1, out_dtype=torch.bfloat16, d=None, accumulate=False):
+    """D = A * B^T with MXFP4 weights b [N, K/2]: A in MXFP4 (a [M, K/2]) or, with a_fmt E4M3, in E4M3 codes
+    [M, K] with 1x128 scales -> D [M, N]."""
+    name = "mxfp4_gemm"
+    M, K = _mxfp4_a(a, sa, a_fmt, name)
+    _check_2d_codes(b, f"{name}: b")
+    N = b.shape[0]
+    if 2 * b.shape[1] != K:
+        raise ValueError(f"{name}: a and b must have the same K")
+    _need(sb, f"{name}: sb", shape=_mxfp4_shapes(N, K)[1], dtype=torch.uint8, contiguous=True)
+    d = _gemm_out(d, M, N, out_dtype, name)
+    _check_dev(a, sa, b, sb, d)
+    if d is None:
+        d = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    _call(name, _ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), M, N, K, _row_ld(a), _row_ld(b), _ptr(d), _dtype_code(d),
+          _row_ld(d), int(bool(accumulate)), _stream(a))
+    return d
+
+
+def mxfp4_grouped_gemm(a, sa, b, sb, group_offsets, a_fmt=E4M3, out_dtype=torch.bfloat16, d=None):
+    """mxfp4_gemm per expert: rows [off[g], off[g+1]) of a [M_cap, ...] with the weights b [G, N, K/2],
+    sb [G, ceil(K/256), N, 8]; offsets int32 [G+1] (device) -> d [M_cap, N]."""
+    name = "mxfp4_grouped_gemm"
+    M_cap, K = _mxfp4_a(a, sa, a_fmt, name)
+    if b.dim() != 3:
+        raise ValueError(f"{name}: b must be [G, N, K/2]")
+    G, N = b.shape[0], b.shape[1]
+    _need(a, f"{name}: a", contiguous=True)
+    _need(b, f"{name}: b", shape=(G, N, K // 2), dtype=torch.uint8, contiguous=True)
+    _need(sb, f"{name}: sb", shape=(G,) + _mxfp4_shapes(N, K)[1], dtype=torch.uint8, contiguous=True)
+    _need(group_offsets, f"{name}: group_offsets", shape=(G + 1,), dtype=torch.int32, contiguous=True)
+    d = _gemm_out(d, M_cap, N, out_dtype, name, contiguous=True)
+    _check_dev(a, sa, b, sb, group_offsets, d)
+    if d is None:
+        d = torch.empty((M_cap, N), dtype=out_dtype, device=a.device)
+    _call(name, _ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), _ptr(group_offsets), G, M_cap, N, K, _ptr(d),
+          _dtype_code(d), _stream(a))
+    return d
+
+
+def moe_router_workspace_size(T, E):
+    return int(_lib.moe_router_workspace_size(T, E))
+
+
+def _router_logits(logits, topk, name):
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"{name}: logits must be [T, E] with unit column stride")
+    T, E = logits.shape
+    if not 1 <= topk <= min(E, 64):
+        raise ValueError(f"{name}: topk must be in [1, min(E, 64)], got {topk}")
+    return T, E, _dtype_code(logits)
+
+
+def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss_coef=0.0, token_mask=None,
+               workspace=None):
+    """Top-k routing of logits [T, E] (fp32/bf16): -> (topk_idx int32 [T, topk], weights fp32 [T, topk],
+    counts int32 [E+1], loss fp32 scalar, or None with loss_coef 0).
+
+    counts[e] is the number of slots that chose expert e, counts[E] the number of live tokens; token_mask
+    (bool or uint8 [T]) marks padding tokens with 0.  Slots without an expert hold id -1 and weight 0."""
+    name = "moe_router"
+    T, E, dt = _router_logits(logits, topk, name)
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"{name}: token_mask must be bool or uint8")
+        _need(token_mask, f"{name}: token_mask", shape=(T,), contiguous=True)
+    if workspace is not None:
+        _need(workspace, f"{name}: workspace", dtype=torch.uint8, contiguous=True)
+    dev = _check_dev(logits, token_mask, workspace)
+    if workspace is None:
+        workspace = torch.empty(max(moe_router_workspace_size(T, E), 4), dtype=torch.uint8, device=dev)
+    idx = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef else None
+    _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(token_mask), score, int(bool(renorm)), scale,
+          loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(workspace), workspace.numel(),
+          _stream(logits))
+    return idx, weights, counts, loss
+
+
+def moe_router_backward(logits, topk_idx, counts, dweights=None, dloss=None, score=ROUTER_SOFTMAX, renorm=False,
+                        scale=1.0, loss_coef=0.0):
+    """Gradient of moe_router's logits from dweights fp32 [T, topk] and dloss (fp32 scalar tensor), either or both;
+    topk_idx and counts are the forward's -> dlogits [T, E] in the logits' dtype."""
+    name = "moe_router_backward"
+    if topk_idx.dim() != 2:
+        raise ValueError(f"{name}: topk_idx must be [T, topk]")
+    topk = topk_idx.shape[1]
+    T, E, dt = _router_logits(logits, topk, name)
+    _need(topk_idx, f"{name}: topk_idx", shape=(T, topk), dtype=torch.int32, contiguous=True)
+    _need(counts, f"{name}: counts", shape=(E + 1,), dtype=torch.int32, contiguous=True)
+    if dweights is not None:
+        _need(dweights, f"{name}: dweights", shape=(T, topk), dtype=torch.float32, contiguous=True)
+    if dloss is not None:
+        _need(dloss, f"{name}: dloss", dtype=torch.float32)
+        if dloss.numel() != 1:
+            raise ValueError(f"{name}: dloss must hold one value")
+    _check_dev(logits, topk_idx, counts, dweights, dloss)
+    dz = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(topk_idx), _ptr(counts), _ptr(dweights),
+          _ptr(dloss), score, int(bool(renorm)), scale, loss_coef, _ptr(dz), E, _stream(logits))
+    return dz

@@ -63,6 +63,8 @@ extern "C" {
 #define FGB_E4M3 0 /* OCP E4M3FN: bias 7, max 448, no Inf (the path's default) */
 #define FGB_E5M2 1 /* OCP E5M2: bias 15, max 57344, Inf/NaN at exponent field 31 */
 
+#define FGB_E2M1 2 /* OCP E2M1 (MXFP4): 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two codes to a byte */
+
 /* scale rules of the format-variant entry points */
 #define FGB_SCALE_CEIL 0      /* smallest e with amax <= max * 2^e (the rule everywhere else) */
 #define FGB_SCALE_OCP_FLOOR 1 /* MX standard: e = floor(log2 amax) - emax (8 for E4M3, 15 for E5M2);
@@ -72,6 +74,10 @@ extern "C" {
 #define FGB_ROW1x128 0 /* one scale per row per 128 columns: s[rows, cols/128] */
 #define FGB_ROW1x32 1  /* one scale per row per 32 columns:  s[rows, cols/32] */
 #define FGB_BLOCK128 2 /* one scale per 128x128 block: s[ceil(rows/128), cols/128] */
+
+/* scores of the MoE router */
+#define FGB_ROUTER_SOFTMAX 0
+#define FGB_ROUTER_SIGMOID 1
 
 /* Thread-local text of the last error raised on this thread ("" if none). */
 const char *fgb_last_error(void);
@@ -571,6 +577,121 @@ int mx2_dequant(const uint8_t *q, const uint8_t *s2, const float *s1, int64_t R,
  * One kernel on `stream`; FGB_EINVAL / FGB_EUNSUPPORTED on bad arguments.
  */
 int fgb_hbm_probe(const void *src, void *dst, int64_t rows, int64_t cols, int pattern, void *stream);
+
+/*
+ * MXFP4 tensors ([LP] 2 format table, 5 MX formats: 32 elements share an E8M0
+ * scale).  Codes: E2M1, two to a byte, the even column in the low half, so a row
+ * of cols elements takes cols/2 bytes.  Scales: one byte b = e + 127 per row and 32
+ * columns, stored step-major, s[ceil(cols/256), rows, 8]: byte j of entry (i, r)
+ * belongs to columns 256 i + 32 j .. + 31 of row r, and the bytes of groups past
+ * the last column are 0.  (A tile's scales for 256 columns are thus one run; a
+ * row-major [rows, cols/32] tensor converts by padding its columns to a multiple
+ * of 8, viewing it as [rows, ceil(cols/256), 8] and exchanging the first two
+ * dimensions.)  Byte 255 is E8M0's NaN: the group's values are NaN.
+ */
+
+/*
+ * mxfp4_quant -- MXFP4 quantization of the rows of G stacked matrices.
+ *   x     [G, rows, cols], row stride ldx, matrices rows * ldx apart, FGB_F32 or
+ *         FGB_BF16; cols % 32 == 0
+ *   rule  FGB_SCALE_CEIL: the smallest e with amax <= 6 * 2^e; FGB_SCALE_OCP_FLOOR:
+ *         e = floor(log2 amax) - 2, elements above 6 * 2^e clip to it.  e >= -127.
+ *   q     [G, rows, cols/2], s [G, ceil(cols/256), rows, 8] dense.  A code is E2M1 of x * 2^-e, round to
+ *         nearest even, sign kept; a group with an infinity or NaN gets byte 255.
+ */
+int mxfp4_quant(const void *x, int x_dtype, int G, int64_t rows, int64_t cols, int64_t ldx, int rule, uint8_t *q,
+                uint8_t *s, void *stream);
+
+/*
+ * mxfp4_quant_t -- mxfp4_quant of x and of each matrix's transpose from one read: the
+ * two copies a training step's three products need (Fprop and Dgrad contract
+ * over the columns, Wgrad over the rows, [DSV3] 1).
+ *   q, s    as mxfp4_quant
+ *   qt, st  the transposes, [G, cols, R] with R = rows rounded up to 32: codes
+ *           [G, cols, R/2], scales [G, ceil(R/256), cols, 8]; columns >= rows hold code 0,
+ *           and the last group's scale comes from the rows that exist.
+ * rows below 2^23.
+ */
+int mxfp4_quant_t(const void *x, int x_dtype, int G, int64_t rows, int64_t cols, int64_t ldx, int rule, uint8_t *q,
+                  uint8_t *s, uint8_t *qt, uint8_t *st, void *stream);
+
+/* mxfp4_dequant -- decode(q) * 2^(s - 127) into out [rows, cols] dense, FP32 or BF16 (nearest even). */
+int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols, void *out, int out_dtype,
+                  void *stream);
+
+/*
+ * mxfp4_gemm -- D = A * B^T with MXFP4 weights, FP32 sums.
+ *   a, sa, a_fmt : FGB_E2M1: MXFP4, codes [M, K/2] (ld lda bytes), K % 32 == 0;
+ *                  FGB_E4M3: codes [M, K] (ld lda bytes) with 1x128 scales sa
+ *                  [M, K/128] (dense), as fp8_quant_rowwise, permute_pad and
+ *                  swiglu_quant write them, K % 128 == 0.
+ *   b, sb        : MXFP4, codes [N, K/2] (ld ldb bytes).
+ *   d, d_dtype   : D [M, N], ld ldd, FGB_F32 or FGB_BF16 (round to nearest even);
+ *                  FP32 output needs ldd < 2^23 (else FGB_EUNSUPPORTED);
+ *                  accumulate != 0 (FP32 only): D += A * B^T.
+ * M, N >= 0 (0: nothing is written); K = 0: D = 0 (or unchanged when
+ * accumulating).  lda and ldb multiples of 16 below 2^24; a, b, sb and an MXFP4
+ * sa 16-byte aligned, an E4M3 A's scales and D at their element's size.  With an
+ * E4M3 A each code times its scale becomes a bf16 (exact wherever the value has a
+ * bf16 representation) and products are exact; with an MXFP4 A the matrix unit
+ * takes codes and scales, its sums measured at FP32 rounding.  Results do not
+ * depend on M: a row comes out the same in any batch that takes the same kernel.
+ */
+int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b, const uint8_t *sb, int64_t M, int64_t N,
+               int64_t K, int64_t lda, int64_t ldb, void *d, int d_dtype, int64_t ldd, int accumulate, void *stream);
+
+/*
+ * mxfp4_grouped_gemm -- mxfp4_gemm per expert ([DSV3] 5.6): rows
+ * [off[g], off[g+1]) of A with expert g's weights.
+ *   a  [M_cap, K/2] or [M_cap, K] dense, scales as for mxfp4_gemm (an MXFP4 A's
+ *      scales are [ceil(K/256), M_cap, 8])
+ *   b  [G, N, K/2], sb [G, ceil(K/256), N, 8] dense
+ *   group_offsets : device int32 [G+1], non-decreasing, off[G] <= M_cap, as
+ *      permute_pad writes it; segments need not be padded.  Read on the device.
+ *   d  [M_cap, N] dense (FP32: N < 2^23); rows >= off[G] are neither read nor written.
+ * 1 <= G <= 1024.
+ */
+int mxfp4_grouped_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b, const uint8_t *sb,
+                       const int32_t *group_offsets, int G, int64_t M_cap, int64_t N, int64_t K, void *d, int d_dtype,
+                       void *stream);
+
+/*
+ * moe_router -- the experts of each token, their weights, the slots per expert
+ * and the balance loss, from the router's logits (the topk_idx of permute_pad and
+ * the probs of unpermute_unpad).
+ *   logits      [T, E], row stride ld (elements), FGB_F32 or FGB_BF16, at least
+ *               element-aligned; 1 <= E <= 1024, 1 <= topk <= min(E, 64)
+ *   token_mask  [T] or NULL: 0 marks a padding token
+ *   A token is live if it is not masked and has a logit above -inf.  For live t:
+ *     s = softmax(z) and p = s, or s = sigmoid(z) and p = s / sum s (score);
+ *     topk_idx[t] = the experts of the topk largest logits, largest first, equal
+ *     logits by lowest id; -inf and NaN are never chosen;
+ *     weights[t][j] = scale * s of the j-th, divided by the chosen s's sum if renorm.
+ *   Slots left over, and all slots of a token that is not live: id -1 (which
+ *   permute_pad drops), weight 0.
+ *   counts[e]   = slots that chose e, counts[E] = the live tokens n
+ *   loss        = loss_coef * E / (topk n^2) * sum_e counts[e] sum_t p[t][e] (0 if n = 0);
+ *                 NULL: not computed
+ *   A NaN or +inf logit of a live token makes its weights and the loss NaN.
+ *   workspace: moe_router_workspace_size(T, E) bytes, contents on entry irrelevant.
+ * Sums are fp32 in a fixed order: results are the same on every run.
+ */
+int moe_router(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk, const uint8_t *token_mask,
+               int score, int renorm, float scale, float loss_coef, int32_t *topk_idx, float *weights, int32_t *counts,
+               float *loss, void *workspace, size_t ws_bytes, void *stream);
+size_t moe_router_workspace_size(int64_t T, int E);
+
+/*
+ * moe_router_backward -- the gradient of the logits from dweights [T, topk]
+ * (NULL: zeros) and dloss (device scalar, NULL: 0): scores are recomputed from
+ * the logits, topk_idx and counts are the forward's (counts are constants of the
+ * loss, as usual for this loss).  Gradients of slots with id -1 are ignored;
+ * tokens that were not live get zeros.  dlogits [T, E], row stride ldd, in the
+ * logits' type (BF16: nearest even).  Other arguments as in the forward call.
+ */
+int moe_router_backward(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk, const int32_t *topk_idx,
+                        const int32_t *counts, const float *dweights, const float *dloss, int score, int renorm,
+                        float scale, float loss_coef, void *dlogits, int64_t ldd, void *stream);
 
 #ifdef __cplusplus
 }

@@ -49,7 +49,7 @@ __device__ __forceinline__ uint32_t cvt4_e4m3(float a, float b, float c, float d
 }
 
 // Element formats and scale rules of the format-variant entry points.
-enum { FMT_E4M3 = 0, FMT_E5M2 = 1 };
+enum { FMT_E4M3 = 0, FMT_E5M2 = 1, FMT_E2M1 = 2 };
 enum { RULE_CEIL = 0, RULE_OCP_FLOOR = 1 };
 
 // Scale exponent for an element format and rule.  CEIL: the smallest e with

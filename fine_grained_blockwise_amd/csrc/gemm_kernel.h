@@ -64,20 +64,15 @@ constexpr int BM = 256, BN = 256, BK = 128;
 constexpr int NBUF = 2;                              // ring of K-step (K = 128) buffers
 constexpr int STEP_BYTES = BM * BK;                  // one operand tile of a K step: 32 KB
 constexpr int BUF_BYTES = 2 * STEP_BYTES;            // A and B: 64 KB
-constexpr int SC_SLOT = 2 * 256 * 4;                 // A and B scale tables of one K step: 2 KB
-constexpr int SC_OFF = 0;                             // LDS: scale tables of two K steps,
-constexpr int RING_OFF = 2 * SC_SLOT;                 // then the ring of K-step buffers,
-constexpr int EPI_OFF = RING_OFF + BUF_BYTES;         // the epilogue staging from buffer 1 on
+constexpr int SC_OFF = 0;                             // LDS: scale tables of two K steps, then the ring
 constexpr int EPI_CAP = 8 * 64 * (64 * 2 + 16);       // largest staging (8 waves x 64 rows of 64 bf16): 72 KB
-constexpr int LDS_BYTES = EPI_OFF + EPI_CAP;          // 140 KB
-static_assert(LDS_BYTES >= RING_OFF + NBUF * BUF_BYTES, "the ring fits");
 
 // Word 3 of a raw buffer descriptor on gfx9-family GPUs: 32-bit data format,
 // no swizzle, no index stride (range checks on the byte offset).
 constexpr int BUF_DWORD3 = 0x00020000;
 
-enum { MODE_EXACT = 0, MODE_FAST = 1 };
-enum { AG_ROW128 = 0, AG_ROW32 = 1 };
+enum { MODE_EXACT = 0, MODE_FAST = 1, MODE_FP4 = 2 };
+enum { AG_ROW128 = 0, AG_ROW32 = 1, AG_STEP32 = 2 }; // STEP32: step-major 1x32 scales of an MXFP4 operand
 // dense, M-grouped (experts' rows: contiguous segments, or the masked layout), K-grouped (experts' K ranges)
 enum { GK_NONE = 0, GK_M = 1, GK_K = 2, GK_MM = 3 };
 // Waves per workgroup: one per SIMD (each 128 x 128 of the tile), except the
@@ -87,7 +82,18 @@ enum { GK_NONE = 0, GK_M = 1, GK_K = 2, GK_MM = 3 };
 template <int MODE, int GK> struct Waves {
     static constexpr int NW = MODE == MODE_EXACT && GK == GK_MM ? 8 : 4;
 };
-enum { BG_ROW128 = 0, BG_ROW32 = 1, BG_BLOCK = 2 };
+enum { BG_ROW128 = 0, BG_ROW32 = 1, BG_BLOCK = 2, BG_STEP32 = 3 };
+
+// LDS layout of a mode: the A and B scale tables of two K steps (4 bytes a row and
+// step, or 8 with two MXFP4 operands, whose steps span 256 elements), the ring of
+// K-step buffers, and the epilogue staging over the ring from buffer 1 on.
+template <int MODE> struct Lds {
+    static constexpr int SC_SLOT = 2 * 256 * (MODE == MODE_FP4 ? 8 : 4); // tables of one K step
+    static constexpr int RING_OFF = 2 * SC_SLOT;
+    static constexpr int EPI_OFF = RING_OFF + BUF_BYTES;
+    static constexpr int BYTES = EPI_OFF + EPI_CAP; // 140 or 144 KB
+    static_assert(BYTES >= RING_OFF + NBUF * BUF_BYTES, "the ring fits");
+};
 
 struct GemmArgs {
     const uint8_t *a, *sa, *b, *sb;
@@ -255,6 +261,26 @@ __device__ __forceinline__ v8bf cvt8_bf16_e5m2(uint32_t w0, uint32_t w1, float s
 // is exact wherever code * 2^(byte - 127) has a bf16 representation).
 __device__ __forceinline__ float scale_f32(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// 8 E2M1 codes (one word) -> one 8-element bf16 operand, each value times 2^e (exact).
+__device__ __forceinline__ v8bf cvt8_bf16_e2m1(uint32_t w, float sc)
+{
+    uint4 a;
+    a.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0));
+    a.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1));
+    a.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2));
+    a.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3));
+    return __builtin_bit_cast(v8bf, a);
+}
+
+// One 32x32x64 product of E2M1 codes; BYTE: the scale words' byte to use.
+template <int BYTE>
+__device__ __forceinline__ v16f mfma_fp4(uint4 a, uint4 b, v16f c, uint32_t sa, uint32_t sb)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        (v8i){(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0},
+        (v8i){(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0}, c, 4, 4, BYTE, (int)sa, BYTE, (int)sb);
+}
+
 __device__ __forceinline__ v8i cat(uint4 x, uint4 y)
 {
     return (v8i){(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
@@ -269,7 +295,8 @@ __device__ __forceinline__ v16f mfma_scaled(v8i a, v8i b, v16f c, uint32_t sa, u
 
 // AF: element format of A's codes (FMT_E4M3, or FMT_E5M2 for gradients).
 // ACC: FP32 out, D += the product (dense and K-grouped forms only).
-template <int MODE, int AG, int BG, bool OUT_BF16, int GK, int AF = FMT_E4M3, bool ACC = false>
+// BF: element format of B's codes (FMT_E4M3, or FMT_E2M1 with BG_STEP32 scales).
+template <int MODE, int AG, int BG, bool OUT_BF16, int GK, int AF = FMT_E4M3, bool ACC = false, int BF = FMT_E4M3>
 __global__ __launch_bounds__((Waves<MODE, GK>::NW * 64)) __attribute__((amdgpu_waves_per_eu(Waves<MODE, GK>::NW / 4, Waves<MODE, GK>::NW / 4))) void
 gemm_fp8_kernel(GemmArgs p)
 {
@@ -277,11 +304,19 @@ gemm_fp8_kernel(GemmArgs p)
     // NW waves: a 2 x NW/2 grid of 128 x WNC sub-tiles (TJ column tiles of 32)
     constexpr int NW = Waves<MODE, GK>::NW, WNC = 256 / (NW / 2), TJ = WNC / 32;
     constexpr int RPW = 256 / NW, IPO = RPW / 8; // copy rows and instructions per wave and operand
+    // MXFP4 operands: with both (F4) a K step is 256 elements, 128 bytes a row; with
+    // an E4M3 A (B4) B's rows are 64 bytes of the 128-element step.
+    constexpr bool F4 = MODE == MODE_FP4, B4 = BF == FMT_E2M1 && !F4;
+    static_assert(!F4 || (AF == FMT_E2M1 && BF == FMT_E2M1 && AG == AG_STEP32 && BG == BG_STEP32), "MXFP4 operands");
+    static_assert(!B4 || (MODE == MODE_EXACT && NW == 4 && AG == AG_ROW128 && BG == BG_STEP32), "E4M3 x MXFP4");
+    constexpr int BROW = B4 ? 64 : 128;          // bytes of a B tile row
+    constexpr int IPB = B4 ? IPO / 2 : IPO;      // copy instructions of B per wave
+    constexpr int SC_SLOT = Lds<MODE>::SC_SLOT, RING_OFF = Lds<MODE>::RING_OFF, EPI_OFF = Lds<MODE>::EPI_OFF;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave / (NW / 2), wn = wave % (NW / 2);
     const int l32 = lane & 31, hk = lane >> 5;
     const int64_t K = p.K; // row length of A and B (K-grouped: the whole K capacity)
-    int64_t kbeg = 0, nk = K / BK;
+    int64_t kbeg = 0, nk = F4 ? (K + 2 * BK - 1) / (2 * BK) : K / BK;
     const int64_t N = p.N;
 
     // ---- tile -> (m0, n0) ------------------------------------------------
@@ -370,7 +405,18 @@ gemm_fp8_kernel(GemmArgs p)
         const int64_t br = n0 + r < N ? r : N - 1 - n0;
         a_off[g] = (uint32_t)(ar * p.lda + chunk * 16);
         b_off[g] = (uint32_t)(br * p.ldb + chunk * 16);
+        if constexpr (B4) { // 16 rows of 64 bytes: chunk c of row r at position c ^ (r / 2 % 4)
+            const int rb = wave * RPW + g * 16 + (lane >> 2);
+            const int64_t bc = n0 + rb < N ? rb : N - 1 - n0;
+            b_off[g] = (uint32_t)(bc * p.ldb + ((lane & 3) ^ ((lane >> 3) & 3)) * 16);
+        }
     }
+    // F4 copies are buffer loads, whose range check is per dword and lands zeros in
+    // LDS for what lies outside (measured).  K not a multiple of 256: in the last
+    // step the lanes of chunks past the row's end get an offset past every record
+    // count, so those chunks are zeros.
+    const uint32_t tail_or =
+        F4 && (((lane & 7) ^ swz(lane >> 3)) > (int)((K / 32 - 1) & 7)) ? 0x80000000u : 0u;
     // Scale copy: lane l of wave w fetches the scale of tile row (A) or tile
     // column (B) sw*64 + l for K step ks into dword sw*64 + l of the step's
     // table, sw = w % 4 (with 8 waves, waves 0-3 copy the A scales and waves
@@ -388,10 +434,25 @@ gemm_fp8_kernel(GemmArgs p)
         if constexpr (BG == BG_BLOCK) {
             sb_base = SB;
             sb_off = (uint32_t)(((n0 + c) / 128) * (K / 128));
+        } else if constexpr (BG == BG_STEP32) {
+            sb_base = SB + n0 * 8;
+            sb_off = (uint32_t)(c * 8);
         } else {
             sb_base = SB + n0 * sb_row + kbeg / (B32 ? 32 : 128);
             sb_off = (uint32_t)(c * sb_row);
         }
+    }
+    // F4: a step's scales are 8 bytes a row, rows contiguous; lane l of waves 0, 1
+    // (A) and 2, 3 (B) copies rows 2 l, 2 l + 1 of its half of the tile, zeros past
+    // the operand's last row.
+    const uint32_t sc_off = ((wave & 1) * 128 + 2 * lane) * 8;
+    int sc_rows = 0;
+    int64_t sc_step = BG == BG_STEP32 ? N * 8 : 0; // bytes of a step's scales
+    if constexpr (F4) {
+        const bool is_a = __builtin_amdgcn_readfirstlane(wave) < 2;
+        sc_rows = (int)min((int64_t)256, is_a ? m_end - m0 : N - n0);
+        sa_base = is_a ? p.sa + m0 * 8 : SB + n0 * 8;
+        sc_step = (is_a ? p.M : N) * 8;
     }
 
     // One copy instruction: M0 holds the wave-uniform LDS destination (lane l
@@ -423,16 +484,50 @@ gemm_fp8_kernel(GemmArgs p)
                      : "s"(lds_addr), "v"(off), "s"(uniform(gbase))
                      : "memory", "m0");
     };
+    auto rsrc = [&](const uint8_t *base, int64_t bytes) {
+        const uint8_t *b = uniform(base);
+        return (fgb_u4v){(uint32_t)(uintptr_t)b, (uint32_t)((uintptr_t)b >> 32),
+                         (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), BUF_DWORD3};
+    };
+    auto dma16_buf = [&](fgb_u4v rs, uint32_t off, uint32_t soff, uint32_t lds_addr) {
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(lds_addr), "v"(off), "s"(rs), "s"(soff)
+                     : "memory", "m0");
+    };
     const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
     const uint32_t wave_u = __builtin_amdgcn_readfirstlane(wave);
     const uint8_t *a_base_u = uniform(a_base), *b_base_u = uniform(b_base);
     const uint8_t *sa_base_u = uniform(sa_base), *sb_base_u = uniform(sb_base);
     const int nk32 = (int)nk; // K steps (K < 2^24)
+    fgb_u4v a_rs = {}, b_rs = {}; // F4: the tiles' rows (the launcher keeps 256 rows below 2^31 bytes)
+    if constexpr (F4) {
+        a_rs = rsrc(a_base, (min((int64_t)256, m_end - m0) - 1) * p.lda + K / 2);
+        b_rs = rsrc(b_base, (min((int64_t)256, N - n0) - 1) * p.ldb + K / 2);
+    }
     // Copy instruction i (0..2*IPO-1: A g=0..IPO-1, then B) of K step k
     // (clamped to the last one: copies past the end rewrite the last step's
     // buffer with the bytes it already holds).
     auto dma_tile = [&](int k, int i) {
         const int kc = k < nk32 ? k : nk32 - 1;
+        if constexpr (F4) {
+            const uint32_t dst = lds_base + RING_OFF + (uint32_t)(kc & 1) * BUF_BYTES + (i >= IPO ? STEP_BYTES : 0) +
+                                 (wave_u * RPW + (i % IPO) * 8) * 128;
+            const uint32_t tail = kc == nk32 - 1 ? tail_or : 0u;
+            if (i < IPO)
+                dma16_buf(a_rs, a_off[i % IPO] | tail, (uint32_t)kc * 128u, dst);
+            else
+                dma16_buf(b_rs, b_off[i % IPO] | tail, (uint32_t)kc * 128u, dst);
+            return;
+        }
+        if constexpr (B4) {
+            if (i >= IPO) {
+                const uint32_t dst = lds_base + RING_OFF + (uint32_t)(kc & 1) * BUF_BYTES + STEP_BYTES +
+                                     (wave_u * RPW + (i - IPO) * 16) * 64;
+                dma16(b_base_u + (uint32_t)kc * 64u, b_off[i - IPO], dst);
+                return;
+            }
+        }
         const uint32_t dst = lds_base + RING_OFF + (uint32_t)(kc & 1) * BUF_BYTES + (i >= IPO ? STEP_BYTES : 0) +
                              (wave_u * RPW + (i % IPO) * 8) * 128;
         if (i < IPO)
@@ -446,7 +541,13 @@ gemm_fp8_kernel(GemmArgs p)
         const int kc = ks < nk32 ? ks : nk32 - 1;
         const uint32_t dst = lds_base + SC_OFF + (uint32_t)(kc & 1) * SC_SLOT + (wave_u & 3) * 256;
         const uint32_t ka = A32 ? (uint32_t)kc * 4u : (uint32_t)kc, kb = B32 ? (uint32_t)kc * 4u : (uint32_t)kc;
-        if constexpr (NW == 4) {
+        if constexpr (F4) {
+            dma16_buf(rsrc(sa_base_u + kc * sc_step, sc_rows * 8), sc_off, 0,
+                      lds_base + SC_OFF + (uint32_t)(kc & 1) * SC_SLOT + wave_u * 1024);
+        } else if constexpr (B4) {
+            dma1(sa_base_u + ka, sa_off, dst);
+            dma4(sb_base_u + (kc >> 1) * sc_step + (kc & 1) * 4, sb_off, dst + 1024);
+        } else if constexpr (NW == 4) {
             if constexpr (A32)
                 dma4(sa_base_u + ka, sa_off, dst);
             else
@@ -471,6 +572,12 @@ gemm_fp8_kernel(GemmArgs p)
     auto dma_step = [&](int k, int first, int last) {
         if (first == 0)
             dma_scales(k);
+        if constexpr (F4) {
+#pragma unroll
+            for (int i = first; i <= last; i++)
+                dma_tile(k, i);
+            return;
+        }
         for (int i = first; i <= last; i++)
             dma_tile(k, i);
     };
@@ -486,7 +593,9 @@ gemm_fp8_kernel(GemmArgs p)
     // packed for 1x128 into one word with byte t = tile t; likewise B (TJ
     // tiles), whose 128x128 form is one byte (the wave's columns lie in one
     // block).
-    constexpr int NA = A32 ? 4 : 1, NB = B32 ? TJ : 1;
+    // F4: the two words of each tile's row are kept apart (word w: chunks 4w .. 4w+3),
+    // shifted down by the lane half, so that bytes 0 and 2 are the lane's scales.
+    constexpr int NA = A32 || F4 ? 4 : 1, NB = B32 || B4 || F4 ? TJ : 1;
     // read_scales issues the LDS reads (raw dwords); pack_scales combines them
     // and is placed a few slots later so the reads have landed by then.
     auto read_scales = [&](int ks, uint32_t(&va)[4], uint32_t(&vb)[4]) {
@@ -506,7 +615,7 @@ gemm_fp8_kernel(GemmArgs p)
         } else {
             wa[0] = va[0] | (va[1] << 8) | (va[2] << 16) | (va[3] << 24);
         }
-        if constexpr (B32) {
+        if constexpr (B32 || B4) {
 #pragma unroll
             for (int t = 0; t < TJ; t++)
                 wb[t] = vb[t];
@@ -526,7 +635,7 @@ gemm_fp8_kernel(GemmArgs p)
     for (int c = 0; c < 8; c++)
         qoff[c] = l32 * 128 + ((c ^ swz(l32)) * 16);
     auto lds_a = [&](int k) { return smem + RING_OFF + (k & 1) * BUF_BYTES + wm * 128 * 128; };
-    auto lds_b = [&](int k) { return smem + RING_OFF + (k & 1) * BUF_BYTES + STEP_BYTES + wn * WNC * 128; };
+    auto lds_b = [&](int k) { return smem + RING_OFF + (k & 1) * BUF_BYTES + STEP_BYTES + wn * WNC * BROW; };
 
     v16f acc[4][TJ];
 #pragma unroll
@@ -539,10 +648,18 @@ gemm_fp8_kernel(GemmArgs p)
     // ---- prologue ----------------------------------------------------------------
     // Step 0 and the first part of step 1 in flight (the rest of step 1 is
     // issued in the first slots of the main loop); wait for step 0 and sync.
-    if constexpr (MODE == MODE_FAST) {
+    if constexpr (F4) {
+        dma_step(0, 0, 2 * IPO - 1);
+        dma_step(1, 0, 11);
+        FGB_WAIT_SYNC(13); // step 1's scale and 12 tile instructions
+    } else if constexpr (MODE == MODE_FAST) {
         dma_step(0, 0, 2 * IPO - 1);
         dma_step(1, 0, 11);
         FGB_WAIT_SYNC(14); // step 1's two scale and 12 tile instructions
+    } else if constexpr (B4) {
+        dma_step(0, 0, IPO + IPB - 1);
+        dma_step(1, 0, 5);
+        FGB_WAIT_SYNC(8); // step 1's two scale and 6 tile instructions
     } else if constexpr (NW == 4) {
         dma_step(0, 0, 2 * IPO - 1);
         dma_step(1, 0, 7);
@@ -553,15 +670,119 @@ gemm_fp8_kernel(GemmArgs p)
         FGB_WAIT_SYNC(4); // step 1's scale and 3 tile instructions
     }
     uint32_t ca[NA], cb[NB], sva[4], svb[4];
-    read_scales(0, sva, svb);
-    pack_scales(sva, svb, ca, cb);
+    if constexpr (!F4) {
+        read_scales(0, sva, svb);
+        pack_scales(sva, svb, ca, cb);
+    }
 
     // ---- main loop ----------------------------------------------------------------
     // A K step is 8 slots.  One barrier per step waits for step ks+1's copies
     // (all issued at least four slots earlier) before its first reads and
     // frees buffer ks % 2 (every wave has issued its last read of step ks);
     // step ks+2's copies go out right after the barrier that frees its buffer.
-    if constexpr (MODE == MODE_FAST) {
+    if constexpr (F4) {
+        // As the fast mode below, with 128 bytes a row holding 256 elements: a
+        // half-step's two chunks feed two 32x32x64 matrix instructions, lane half hk
+        // taking chunks 4hs+hk and 4hs+2+hk with their own scale bytes.  One step's
+        // 64 instructions of 32 cycles read what the fast mode's 32 of 64 cycles read.
+        uint4 f[2][2][4][2];         // [half][A/B][tile][chunk]
+        uint32_t xa[4][2], xb[4][2]; // scale words of this step, by tile and half-step
+        uint2 va[4], vb[4];          // of the next one, as read
+        auto read_frag = [&](int k, int hs, int op, uint4(&x)[4][2]) {
+            const uint8_t *base = op == 0 ? lds_a(k) : lds_b(k);
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                x[t][0] = *reinterpret_cast<const uint4 *>(base + qoff[4 * hs + hk] + t * 4096);
+                x[t][1] = *reinterpret_cast<const uint4 *>(base + qoff[4 * hs + 2 + hk] + t * 4096);
+            }
+        };
+        auto read_scales4 = [&](int ks) {
+            const uint8_t *ta = smem + SC_OFF + (ks & 1) * SC_SLOT, *tb = ta + 2048;
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                va[t] = *reinterpret_cast<const uint2 *>(ta + (wm * 128 + t * 32 + l32) * 8);
+                vb[t] = *reinterpret_cast<const uint2 *>(tb + (wn * 128 + t * 32 + l32) * 8);
+            }
+        };
+        auto pack_scales4 = [&]() {
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                xa[t][0] = va[t].x >> (8 * hk);
+                xa[t][1] = va[t].y >> (8 * hk);
+                xb[t][0] = vb[t].x >> (8 * hk);
+                xb[t][1] = vb[t].y >> (8 * hk);
+            }
+        };
+        auto mfma_row = [&](int hs, int i, const uint4(&a)[4][2], const uint4(&b)[4][2]) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                acc[i][j] = mfma_fp4<0>(a[i][0], b[j][0], acc[i][j], xa[i][hs], xb[j][hs]);
+                acc[i][j] = mfma_fp4<2>(a[i][1], b[j][1], acc[i][j], xa[i][hs], xb[j][hs]);
+            }
+        };
+        read_scales4(0);
+        pack_scales4();
+        read_frag(0, 0, 0, f[0][0]);
+        read_frag(0, 0, 1, f[0][1]);
+#define FGB_PACE()                                                                                                     \
+    do {                                                                                                               \
+        for (int k_ = 0; k_ < 8; k_++) {                                                                               \
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); /* 1 MFMA */                                            \
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0); /* 1 LDS read */                                        \
+        }                                                                                                              \
+        __builtin_amdgcn_sched_barrier(0);                                                                             \
+    } while (0)
+        for (int ks = 0; ks < nk32; ks++) {
+            // slot 0
+            dma_tile(ks + 1, 12);
+            dma_tile(ks + 1, 13);
+            mfma_row(0, 0, f[0][0], f[0][1]);
+            __builtin_amdgcn_sched_barrier(0);
+            // slot 1
+            dma_tile(ks + 1, 14);
+            dma_tile(ks + 1, 15);
+            read_frag(ks, 1, 0, f[1][0]);
+            mfma_row(0, 1, f[0][0], f[0][1]);
+            FGB_PACE();
+            // slot 2
+            read_frag(ks, 1, 1, f[1][1]);
+            mfma_row(0, 2, f[0][0], f[0][1]);
+            FGB_PACE();
+            // slot 3: every wave's reads of step ks are done -> buffer ks % 2 is free
+            __syncthreads();
+            dma_step(ks + 2, 0, 1);
+            mfma_row(0, 3, f[0][0], f[0][1]);
+            __builtin_amdgcn_sched_barrier(0);
+            // slot 4
+            dma_tile(ks + 2, 2);
+            dma_tile(ks + 2, 3);
+            dma_tile(ks + 2, 4);
+            mfma_row(1, 0, f[1][0], f[1][1]);
+            __builtin_amdgcn_sched_barrier(0);
+            // slot 5: step ks+1 has landed (6 instructions of step ks+2 were issued after it)
+            FGB_WAIT_SYNC(6);
+            read_scales4(ks + 1);
+            dma_tile(ks + 2, 5);
+            dma_tile(ks + 2, 6);
+            dma_tile(ks + 2, 7);
+            read_frag(ks + 1, 0, 0, f[0][0]);
+            mfma_row(1, 1, f[1][0], f[1][1]);
+            FGB_PACE();
+            // slot 6
+            dma_tile(ks + 2, 8);
+            dma_tile(ks + 2, 9);
+            read_frag(ks + 1, 0, 1, f[0][1]);
+            mfma_row(1, 2, f[1][0], f[1][1]);
+            FGB_PACE();
+            // slot 7: the next step's scales replace the current ones after this slot's MFMAs
+            dma_tile(ks + 2, 10);
+            dma_tile(ks + 2, 11);
+            mfma_row(1, 3, f[1][0], f[1][1]);
+            pack_scales4();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#undef FGB_PACE
+    } else if constexpr (MODE == MODE_FAST) {
         // A half-step (64 of the step's 128 K) is one MFMA sub-step: 16 scaled
         // MFMAs, 4 per slot.  Lane half hk reads chunks 4hs+hk and 4hs+2+hk of
         // each tile row for half hs (hardware K blocks 0 and 1).  Half 1 of
@@ -682,6 +903,135 @@ gemm_fp8_kernel(GemmArgs p)
             pack_scales(sva, svb, ca, cb);
             __builtin_amdgcn_sched_barrier(0);
         }
+    } else if constexpr (B4) {
+        // Exact mode with an MXFP4 B, 4 waves: the slots of the form below, over 64
+        // elements Q (two a step) of 4 sub-steps s each.  Lane half hk takes elements
+        // 32 hk .. 32 hk + 31 of the 64: B's chunk 2Q + hk (one 16-byte read, one
+        // scale), A's chunks 4Q + 2 hk and the next; sub-step s uses B's word s and A's
+        // bytes 8 (s % 2) .. of chunk s / 2.  A unit is two sub-steps (one A chunk).
+        uint4 rA[2][4], rB[2][4]; // FP8 fragments of two units, MXFP4 fragments of two Q
+        v8bf cA[2][4], cB[2][4];  // bf16 operands of two sub-steps
+        float sfA[4], sfB[4];     // scale factors being used for conversion
+        const int bsw = (l32 >> 1) & 3;
+        int qa[4]; // unit u's chunk 4 (u / 2) + 2 hk + u % 2, swizzled
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            qa[u] = l32 * 128 + (((4 * (u >> 1) + 2 * hk + (u & 1)) ^ swz(l32)) * 16);
+        auto factors_a = [&]() {
+#pragma unroll
+            for (int t = 0; t < 4; t++)
+                sfA[t] = scale_f32((ca[0] >> (8 * t)) & 0xFFu);
+        };
+        auto factors_b = [&](int q) {
+#pragma unroll
+            for (int t = 0; t < 4; t++)
+                sfB[t] = scale_f32((cb[t] >> (16 * q + 8 * hk)) & 0xFFu);
+        };
+        // unit u (0..3) of step k: A tile t; Q (0, 1): B tile t
+        auto read_a = [&](int k, int u, int t, uint4(&x)[4]) {
+            x[t] = *reinterpret_cast<const uint4 *>(lds_a(k) + qa[u] + t * 4096);
+        };
+        auto read_b = [&](int k, int q, int t, uint4(&x)[4]) {
+            x[t] = *reinterpret_cast<const uint4 *>(lds_b(k) + l32 * 64 + (((2 * q + hk) ^ bsw) * 16) + t * 2048);
+        };
+        // sub-step s (0..7 of a step) into buffer s % 2 from A fragment xa, B fragment xb
+        auto cvt_piece = [&](int s, int t, const uint4(&xa)[4], const uint4(&xb)[4]) {
+            cA[s & 1][t] = (s & 1) == 0 ? cvt8_bf16(xa[t].x, xa[t].y, sfA[t]) : cvt8_bf16(xa[t].z, xa[t].w, sfA[t]);
+            const uint32_t w = (s & 3) == 0 ? xb[t].x : (s & 3) == 1 ? xb[t].y : (s & 3) == 2 ? xb[t].z : xb[t].w;
+            cB[s & 1][t] = cvt8_bf16_e2m1(w, sfB[t]);
+        };
+        auto mfma_row = [&](int buf, int i) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cA[buf][i], cB[buf][j], acc[i][j], 0, 0, 0);
+        };
+        // quarter T of a slot: row tile T's MFMAs of the sub-step before S, and
+        // piece T of sub-step S's conversions between them
+#define FGB_Q(S, RA, RB, T)                                                                                            \
+    do {                                                                                                               \
+        cvt_piece(S, T, rA[RA], rB[RB]);                                                                               \
+        mfma_row(1 - ((S) & 1), T);                                                                                    \
+        for (int k_ = 0; k_ < 4; k_++) {                                                                               \
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); /* 1 MFMA */                                            \
+            __builtin_amdgcn_sched_group_barrier(0x002, 2, 0); /* 2 VALU */                                            \
+        }                                                                                                              \
+        __builtin_amdgcn_sched_barrier(0);                                                                             \
+    } while (0)
+
+        factors_a();
+        factors_b(0);
+#pragma unroll
+        for (int t = 0; t < 4; t++) {
+            read_a(0, 0, t, rA[0]);
+            read_b(0, 0, t, rB[0]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+            cvt_piece(0, t, rA[0], rB[0]);
+        __builtin_amdgcn_sched_barrier(0);
+        for (int ks = 0; ks < nk32; ks++) {
+            // slot s: MFMAs of sub-step s, conversions of sub-step s + 1
+            // slot 0: unit 1's reads; step ks+1's copies 6-9
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                read_a(ks, 1, t, rA[1]);
+                dma_tile(ks + 1, 6 + t);
+                FGB_Q(1, 0, 0, t);
+            }
+            // slot 1: copies 10, 11
+            dma_tile(ks + 1, 10);
+            FGB_Q(2, 1, 0, 0);
+            dma_tile(ks + 1, 11);
+            FGB_Q(2, 1, 0, 1);
+            FGB_Q(2, 1, 0, 2);
+            FGB_Q(2, 1, 0, 3);
+            // slot 2: unit 2's reads (A and Q 1's B)
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                read_a(ks, 2, t, rA[0]);
+                read_b(ks, 1, t, rB[1]);
+                FGB_Q(3, 1, 0, t);
+            }
+            // slot 3
+            factors_b(1);
+#pragma unroll
+            for (int t = 0; t < 4; t++)
+                FGB_Q(4, 0, 1, t);
+            // slot 4: unit 3's reads
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                read_a(ks, 3, t, rA[1]);
+                FGB_Q(5, 0, 1, t);
+            }
+            // slot 5
+#pragma unroll
+            for (int t = 0; t < 4; t++)
+                FGB_Q(6, 1, 1, t);
+            // slot 6: step ks+1 has landed (nothing issued after it) and buffer ks % 2
+            // is free; step ks+1's scales and unit 0, step ks+2's scales and copies 0-3.
+            // After the last step these reads touch only LDS and are discarded.
+            FGB_WAIT_SYNC(0);
+            read_scales(ks + 1, sva, svb);
+            dma_scales(ks + 2);
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                read_a(ks + 1, 0, t, rA[0]);
+                read_b(ks + 1, 0, t, rB[0]);
+                dma_tile(ks + 2, t);
+                FGB_Q(7, 1, 1, t);
+            }
+            // slot 7: step ks+1's scales replace the current ones; copies 4, 5
+            pack_scales(sva, svb, ca, cb);
+            factors_a();
+            factors_b(0);
+            dma_tile(ks + 2, 4);
+            FGB_Q(0, 0, 0, 0);
+            dma_tile(ks + 2, 5);
+            FGB_Q(0, 0, 0, 1);
+            FGB_Q(0, 0, 0, 2);
+            FGB_Q(0, 0, 0, 3);
+        }
+#undef FGB_Q
     } else if constexpr (NW == 4) {
         // Exact mode, 4 waves (one per SIMD, each 128 x 128).  A slot is one
         // 16-deep sub-step s: its 16 bf16 MFMAs, with the 32 conversions of
@@ -1173,10 +1523,10 @@ gemm_fp8_kernel(GemmArgs p)
     }
 }
 
-template <int MODE, int AG, int BG, bool OUT_BF16, int GK, int AF = FMT_E4M3, bool ACC = false>
+template <int MODE, int AG, int BG, bool OUT_BF16, int GK, int AF = FMT_E4M3, bool ACC = false, int BF = FMT_E4M3>
 static int launch_one(const GemmArgs &p, int64_t grid, hipStream_t st)
 {
-    auto kern = gemm_fp8_kernel<MODE, AG, BG, OUT_BF16, GK, AF, ACC>;
+    auto kern = gemm_fp8_kernel<MODE, AG, BG, OUT_BF16, GK, AF, ACC, BF>;
     // FP32 output: the epilogue's buffer offsets stay below 2^31 for rows up to 2^23 elements
     if (!OUT_BF16 && p.ldd >= ((int64_t)1 << 23))
         return set_error(FGB_EUNSUPPORTED, "gemm: FP32 output rows (ldd) must be shorter than 2^23 elements");
@@ -1189,29 +1539,30 @@ static int launch_one(const GemmArgs &p, int64_t grid, hipStream_t st)
         dev = -1;
     const bool cached = dev >= 0 && dev < 64;
     if (!cached || !attr_set[dev].load(std::memory_order_acquire)) {
-        hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
+        hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           Lds<MODE>::BYTES);
         if (e != hipSuccess)
             return set_error(FGB_EHIP, "gemm: hipFuncSetAttribute failed: %s", hipGetErrorString(e));
         if (cached)
             attr_set[dev].store(true, std::memory_order_release);
     }
-    kern<<<(unsigned)grid, Waves<MODE, GK>::NW * 64, LDS_BYTES, st>>>(p);
+    kern<<<(unsigned)grid, Waves<MODE, GK>::NW * 64, Lds<MODE>::BYTES, st>>>(p);
     FGB_LAUNCHED("gemm_fp8_kernel");
     return FGB_OK;
 }
 
 // The instantiation for the output type and, with FP32 output in the dense
 // and K-grouped forms, accumulation into D.
-template <int MODE, int AG, int BG, int GK, int AF = FMT_E4M3>
+template <int MODE, int AG, int BG, int GK, int AF = FMT_E4M3, int BF = FMT_E4M3>
 static int launch_out(bool bf16, const GemmArgs &p, int64_t grid, hipStream_t st)
 {
     if (bf16)
-        return launch_one<MODE, AG, BG, true, GK, AF>(p, grid, st);
+        return launch_one<MODE, AG, BG, true, GK, AF, false, BF>(p, grid, st);
     if constexpr (GK == GK_NONE || GK == GK_K) {
         if (p.accumulate)
-            return launch_one<MODE, AG, BG, false, GK, AF, true>(p, grid, st);
+            return launch_one<MODE, AG, BG, false, GK, AF, true, BF>(p, grid, st);
     }
-    return launch_one<MODE, AG, BG, false, GK, AF>(p, grid, st);
+    return launch_one<MODE, AG, BG, false, GK, AF, false, BF>(p, grid, st);
 }
 
 } // namespace fgb

@@ -8,13 +8,9 @@
 //     2^-20 .. 2^20 apart; scale byte 255 gives NaN).
 //   E4M3 A: both operands become bf16 with their power of two folded in (exact),
 //     multiplied on the bf16 matrix unit with FP32 sums, as FGB_GEMM_EXACT does.
-#include "fgb_internal.h"
+#include "gemm_kernel.h"
 
 namespace fgb {
-
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 struct Mx4Args {
     const uint8_t *a, *sa, *b, *sb;
@@ -24,26 +20,6 @@ struct Mx4Args {
     const int32_t *offs; // grouped: [G + 1], else NULL
     int G;
 };
-
-// 8 E2M1 codes (one word) -> 8 bf16 times the power of two in sc's exponent field.
-__device__ __forceinline__ v8bf e2m1_bf16(uint32_t w, float sc)
-{
-    uint4 a;
-    a.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0));
-    a.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1));
-    a.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2));
-    a.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3));
-    return __builtin_bit_cast(v8bf, a);
-}
-__device__ __forceinline__ v8bf e4m3_bf16(uint32_t w0, uint32_t w1, float sc)
-{
-    uint4 a;
-    a.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, sc, false));
-    a.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, sc, true));
-    a.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, sc, false));
-    a.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, sc, true));
-    return __builtin_bit_cast(v8bf, a);
-}
 
 // One wave per 32 x 32 tile of D, operands straight from memory: lane l holds row
 // l % 32 of both and the 32-element group l / 32 of each 64 columns.
@@ -85,10 +61,10 @@ __global__ __launch_bounds__(64) void mx4_gemm_kernel(Mx4Args p)
                 const uint4 a0 = ap[0], a1 = ap[1];
                 const float fa = __uint_as_float((uint32_t)p.sa[m * (p.K / 128) + gc / 4] << 23);
                 const float fb = __uint_as_float(bs << 23);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_bf16(a0.x, a0.y, fa), e2m1_bf16(bw.x, fb), acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_bf16(a0.z, a0.w, fa), e2m1_bf16(bw.y, fb), acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_bf16(a1.x, a1.y, fa), e2m1_bf16(bw.z, fb), acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_bf16(a1.z, a1.w, fa), e2m1_bf16(bw.w, fb), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a0.x, a0.y, fa), cvt8_bf16_e2m1(bw.x, fb), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a0.z, a0.w, fa), cvt8_bf16_e2m1(bw.y, fb), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a1.x, a1.y, fa), cvt8_bf16_e2m1(bw.z, fb), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a1.z, a1.w, fa), cvt8_bf16_e2m1(bw.w, fb), acc, 0, 0, 0);
             }
         }
         // register i of lane l: row (i / 4) * 8 + (l / 32) * 4 + i % 4, column l % 32
@@ -112,15 +88,37 @@ static int check_mx4(const char *name, int a_fmt, int64_t M, int64_t N, int64_t 
     FGB_REQUIRE(M >= 0 && N >= 0 && K >= 0 && K % (a_fmt == FGB_E4M3 ? 128 : 32) == 0, FGB_EINVAL,
                 "%s: need M, N >= 0 and K a multiple of 32 (128 with an E4M3 A) (M=%lld N=%lld K=%lld)", name,
                 (long long)M, (long long)N, (long long)K);
-    FGB_REQUIRE(M < (1ll << 31) && N < (1ll << 31) && K < (1ll << 24), FGB_EINVAL,
-                "%s: M and N must be below 2^31 and K below 2^24", name);
+    FGB_REQUIRE(M < (1ll << 31) && N < (1ll << 31) && K < (1ll << 23), FGB_EINVAL,
+                "%s: M and N must be below 2^31 and K below 2^23", name);
     FGB_REQUIRE(d_dtype == FGB_F32 || d_dtype == FGB_BF16, FGB_EUNSUPPORTED, "%s: d_dtype must be FGB_F32 or FGB_BF16",
                 name);
     return FGB_OK;
 }
 
+// The 256 x 256-tiled kernel of gemm_kernel.h.
+template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16, hipStream_t st)
+{
+    GemmArgs p{};
+    p.a = x.a; p.sa = x.sa; p.b = x.b; p.sb = x.sb; p.d = x.d;
+    p.M = x.M; p.N = x.N; p.K = x.K; p.lda = x.lda; p.ldb = x.ldb; p.ldd = x.ldd;
+    p.accumulate = x.accumulate;
+    p.tiles_n = (int)((x.N + BN - 1) / BN);
+    p.offs = x.offs;
+    p.G = x.G;
+    p.b_stride = x.N * (x.K / 2);
+    p.sb_stride = (x.K + 255) / 256 * x.N * 8;
+    const int64_t tiles = ((x.M + BM - 1) / BM + (GK == GK_M ? x.G : 0)) * p.tiles_n;
+    FGB_REQUIRE(tiles < (1ll << 31), FGB_EINVAL, "mxfp4 gemm: too many tiles");
+    if (a_fmt == FGB_E4M3)
+        return launch_out<MODE_EXACT, AG_ROW128, BG_STEP32, GK, FMT_E4M3, FMT_E2M1>(bf16, p, tiles, st);
+    return launch_out<MODE_FP4, AG_STEP32, BG_STEP32, GK, FMT_E2M1, FMT_E2M1>(bf16, p, tiles, st);
+}
+
 static int launch_mx4(const char *name, const Mx4Args &p, int a_fmt, int d_dtype, hipStream_t st)
 {
+    if (p.offs ? p.M > 64 * p.G : p.M > 64)
+        return p.offs ? launch_tiled<GK_M>(p, a_fmt, d_dtype == FGB_BF16, st)
+                      : launch_tiled<GK_NONE>(p, a_fmt, d_dtype == FGB_BF16, st);
     const int64_t gx = (p.N + 31) / 32, tiles = (p.M + 31) / 32;
     const dim3 grid((unsigned)gx, (unsigned)(p.offs ? (tiles < 16 ? tiles : 16) : (tiles < 65535 ? tiles : 65535)),
                     (unsigned)p.G);
@@ -153,8 +151,8 @@ extern "C" int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const 
     const int64_t row_a = a_fmt == FGB_E4M3 ? K : K / 2;
     FGB_REQUIRE(K == 0 || (lda >= row_a && ldb >= K / 2 && lda % 16 == 0 && ldb % 16 == 0), FGB_EINVAL,
                 "mxfp4_gemm: lda and ldb (bytes) must hold a row and be multiples of 16");
-    FGB_REQUIRE(K == 0 || (256 * lda < (1ll << 32) && 256 * ldb < (1ll << 32)), FGB_EINVAL,
-                "mxfp4_gemm: lda/ldb too large");
+    FGB_REQUIRE(K == 0 || (lda < (1ll << 23) && ldb < (1ll << 23)), FGB_EINVAL,
+                "mxfp4_gemm: lda and ldb must be below 2^23 bytes");
     FGB_REQUIRE(ldd >= N, FGB_EINVAL, "mxfp4_gemm: ldd must be >= N");
     FGB_REQUIRE(d_dtype == FGB_BF16 || ldd < (1ll << 23), FGB_EUNSUPPORTED,
                 "mxfp4_gemm: FP32 output rows (ldd) must be shorter than 2^23 elements");

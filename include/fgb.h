@@ -630,7 +630,7 @@ int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols
  *                  FP32 output needs ldd < 2^23 (else FGB_EUNSUPPORTED);
  *                  accumulate != 0 (FP32 only): D += A * B^T.
  * M, N >= 0 (0: nothing is written); K = 0: D = 0 (or unchanged when
- * accumulating).  lda and ldb multiples of 16 below 2^24; a, b, sb and an MXFP4
+ * accumulating).  lda and ldb multiples of 16 below 2^23; a, b, sb and an MXFP4
  * sa 16-byte aligned, an E4M3 A's scales and D at their element's size.  With an
  * E4M3 A each code times its scale becomes a bf16 (exact wherever the value has a
  * bf16 representation) and products are exact; with an MXFP4 A the matrix unit

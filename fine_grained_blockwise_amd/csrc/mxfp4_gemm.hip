@@ -21,65 +21,227 @@ struct Mx4Args {
     int G;
 };
 
-// One wave per 32 x 32 tile of D, operands straight from memory: lane l holds row
-// l % 32 of both and the 32-element group l / 32 of each 64 columns.
-template <bool A8, bool OUT_BF16>
-__global__ __launch_bounds__(64) void mx4_gemm_kernel(Mx4Args p)
+// Few rows (decode, short prompts, few rows per expert): the weights' bytes bound
+// it.  A workgroup of W waves owns 16 NB columns of D and 16 MB rows at a time;
+// its waves split K by 256 elements (a 128-byte line of each weight row) and their
+// sums are added through LDS in wave order.  The weights are the first operand of
+// the 16-row matrix instructions and the activations the second, both straight from
+// memory: lane l holds row l % 16 and the 32-element groups l / 16 and 4 + l / 16 of
+// a unit, so a load instruction covers 64 contiguous bytes of 16 rows, and a lane
+// ends with four consecutive columns of one row of D.  The next unit's loads are
+// issued before a unit is multiplied.
+template <bool A8, int MB, int NB> struct NarrowUnit {
+    uint4 b[NB][2], a[MB][A8 ? 4 : 2];
+    uint2 bs[NB], as[MB]; // scale bytes of a row: all eight groups (an E4M3 A: .x holds its two)
+};
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+template <bool A8, int MB, int NB, int W, bool OUT_BF16>
+__global__ __launch_bounds__(W * 64) void mx4_narrow_kernel(Mx4Args p, int tiles_n, int chunks)
 {
-    const int lane = threadIdx.x, r = lane & 31, h = lane >> 5;
-    const int64_t n0 = (int64_t)blockIdx.x * 32;
-    const int e = blockIdx.z;
+    __shared__ v4f part[W][MB * NB][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, h = lane >> 4;
+    // Workgroup -> (column tile, row chunk, expert): eight column tiles, then their
+    // next chunk, so that the chunks of a column tile run on one XCD (b % 8) and
+    // find its weights in that L2.
+    const int64_t per = (int64_t)((tiles_n + 7) / 8) * 8 * chunks;
+    const int e = (int)(blockIdx.x / per);
+    const int64_t in = blockIdx.x % per;
+    const int tn = (int)(in / (8 * chunks)) * 8 + (int)(in & 7), chunk = (int)(in / 8 % chunks);
+    if (tn >= tiles_n)
+        return;
+    const int64_t n0 = (int64_t)tn * (16 * NB);
     int64_t lo = 0, hi = p.M;
     const uint8_t *b = p.b, *sb = p.sb;
-    const int64_t steps = (p.K + 255) / 256;
+    const int units = (int)((p.K + 255) / 256), groups = (int)(p.K / 32);
     if (p.offs) {
         lo = p.offs[e];
         hi = p.offs[e + 1];
         b += (int64_t)e * p.N * p.ldb;
-        sb += (int64_t)e * p.N * steps * 8;
+        sb += (int64_t)e * p.N * units * 8;
     }
-    const int64_t n = n0 + r < p.N ? n0 + r : p.N - 1;
-    for (int64_t m0 = lo + (int64_t)blockIdx.y * 32; m0 < hi; m0 += (int64_t)gridDim.y * 32) {
-        const int64_t m = m0 + r < hi ? m0 + r : hi - 1;
-        v16f acc = {};
-        for (int64_t k = 0; k < p.K; k += 64) {
-            const int64_t g = k / 32 + h; // this lane's group
-            const bool in = g < p.K / 32;
-            const int64_t gc = in ? g : 0;
-            const uint4 bw = *reinterpret_cast<const uint4 *>(b + n * p.ldb + gc * 16);
-            const uint32_t bs = sb[((gc >> 3) * p.N + n) * 8 + (gc & 7)];
-            if constexpr (!A8) {
-                uint4 aw = *reinterpret_cast<const uint4 *>(p.a + m * p.lda + gc * 16);
-                const uint32_t as = p.sa[((gc >> 3) * p.M + m) * 8 + (gc & 7)];
-                if (!in)
-                    aw = make_uint4(0, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    (v8i){(int)aw.x, (int)aw.y, (int)aw.z, (int)aw.w, 0, 0, 0, 0},
-                    (v8i){(int)bw.x, (int)bw.y, (int)bw.z, (int)bw.w, 0, 0, 0, 0}, acc, 4, 4, 0, (int)as, 0, (int)bs);
-            } else {
-                const uint4 *ap = reinterpret_cast<const uint4 *>(p.a + m * p.lda + gc * 32);
-                const uint4 a0 = ap[0], a1 = ap[1];
-                const float fa = __uint_as_float((uint32_t)p.sa[m * (p.K / 128) + gc / 4] << 23);
-                const float fb = __uint_as_float(bs << 23);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a0.x, a0.y, fa), cvt8_bf16_e2m1(bw.x, fb), acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a0.z, a0.w, fa), cvt8_bf16_e2m1(bw.y, fb), acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a1.x, a1.y, fa), cvt8_bf16_e2m1(bw.z, fb), acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(cvt8_bf16(a1.z, a1.w, fa), cvt8_bf16_e2m1(bw.w, fb), acc, 0, 0, 0);
-            }
-        }
-        // register i of lane l: row (i / 4) * 8 + (l / 32) * 4 + i % 4, column l % 32
+    const uint8_t *brow[NB], *bsrow[NB];
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int64_t row = m0 + (i / 4) * 8 + h * 4 + i % 4;
-            if (row < hi && n0 + r < p.N) {
-                const int64_t at = row * p.ldd + n0 + r;
-                if constexpr (OUT_BF16)
-                    ((__bf16 *)p.d)[at] = (__bf16)acc[i];
-                else
-                    ((float *)p.d)[at] = p.accumulate ? ((float *)p.d)[at] + acc[i] : acc[i];
+    for (int j = 0; j < NB; j++) {
+        const int64_t n = n0 + j * 16 + r < p.N ? n0 + j * 16 + r : p.N - 1;
+        brow[j] = b + n * p.ldb + h * 16;
+        bsrow[j] = sb + n * 8;
+    }
+    for (int64_t m0 = lo + (int64_t)chunk * (16 * MB); m0 < hi; m0 += (int64_t)chunks * (16 * MB)) {
+        const uint8_t *arow[MB], *asrow[MB];
+#pragma unroll
+        for (int i = 0; i < MB; i++) {
+            const int64_t m = m0 + i * 16 + r < hi ? m0 + i * 16 + r : hi - 1;
+            arow[i] = p.a + m * p.lda + h * (A8 ? 32 : 16);
+            asrow[i] = A8 ? p.sa + m * (p.K / 128) : p.sa + m * 8;
+        }
+        v4f acc[MB][NB];
+#pragma unroll
+        for (int i = 0; i < MB; i++)
+#pragma unroll
+            for (int j = 0; j < NB; j++)
+                acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+        // A group past K reads bytes of the row's first unit instead; product() then
+        // takes zeros for A (not here: nothing may wait for a load where it is issued).
+        auto load = [&](int u, NarrowUnit<A8, MB, NB> &x) {
+            const bool in0 = u * 8 + h < groups, in1 = u * 8 + 4 + h < groups;
+            const int64_t u0 = in0 ? (int64_t)u * 128 : -(int64_t)h * 16, u1 = in1 ? (int64_t)u * 128 + 64 : -(int64_t)h * 16;
+#pragma unroll
+            for (int j = 0; j < NB; j++) {
+                x.b[j][0] = *reinterpret_cast<const uint4 *>(brow[j] + u0);
+                x.b[j][1] = *reinterpret_cast<const uint4 *>(brow[j] + u1);
+                x.bs[j] = *reinterpret_cast<const uint2 *>(bsrow[j] + (int64_t)u * p.N * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < MB; i++) {
+                if constexpr (A8) {
+                    const uint4 *q0 = reinterpret_cast<const uint4 *>(arow[i] + 2 * u0);
+                    const uint4 *q1 = reinterpret_cast<const uint4 *>(arow[i] + 2 * u1);
+                    x.a[i][0] = q0[0];
+                    x.a[i][1] = q0[1];
+                    x.a[i][2] = q1[0];
+                    x.a[i][3] = q1[1];
+                    x.as[i].x = asrow[i][2 * u];
+                    x.as[i].y = asrow[i][in1 ? 2 * u + 1 : 2 * u];
+                } else {
+                    x.a[i][0] = *reinterpret_cast<const uint4 *>(arow[i] + u0);
+                    x.a[i][1] = *reinterpret_cast<const uint4 *>(arow[i] + u1);
+                    x.as[i] = *reinterpret_cast<const uint2 *>(asrow[i] + (int64_t)u * p.M * 8);
+                }
+            }
+        };
+        auto product = [&](int u, NarrowUnit<A8, MB, NB> &x) {
+            if (u * 8 + 8 > groups) { // uniform: the last unit of a K that is no multiple of 256
+                const bool in0 = u * 8 + h < groups, in1 = u * 8 + 4 + h < groups;
+                constexpr int Q = A8 ? 2 : 1;
+#pragma unroll
+                for (int i = 0; i < MB; i++)
+#pragma unroll
+                    for (int q = 0; q < Q; q++) {
+                        if (!in0)
+                            x.a[i][q] = make_uint4(0, 0, 0, 0);
+                        if (!in1)
+                            x.a[i][Q + q] = make_uint4(0, 0, 0, 0);
+                    }
+            }
+            if constexpr (!A8) {
+#pragma unroll
+                for (int half = 0; half < 2; half++)
+#pragma unroll
+                    for (int i = 0; i < MB; i++)
+#pragma unroll
+                        for (int j = 0; j < NB; j++) {
+                            const uint4 bw = x.b[j][half], aw = x.a[i][half];
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                (v8i){(int)bw.x, (int)bw.y, (int)bw.z, (int)bw.w, 0, 0, 0, 0},
+                                (v8i){(int)aw.x, (int)aw.y, (int)aw.z, (int)aw.w, 0, 0, 0, 0}, acc[i][j], 4, 4, 0,
+                                (int)((half ? x.bs[j].y : x.bs[j].x) >> (8 * h)), 0,
+                                (int)((half ? x.as[i].y : x.as[i].x) >> (8 * h)));
+                        }
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    float fa[MB], fb[NB];
+#pragma unroll
+                    for (int i = 0; i < MB; i++)
+                        fa[i] = scale_f32(half ? x.as[i].y : x.as[i].x);
+#pragma unroll
+                    for (int j = 0; j < NB; j++)
+                        fb[j] = scale_f32(((half ? x.bs[j].y : x.bs[j].x) >> (8 * h)) & 0xFFu);
+#pragma unroll
+                    for (int s = 0; s < 4; s++) {
+                        v8bf bv[NB];
+#pragma unroll
+                        for (int j = 0; j < NB; j++) {
+                            const uint4 w = x.b[j][half];
+                            bv[j] = cvt8_bf16_e2m1(s == 0 ? w.x : s == 1 ? w.y : s == 2 ? w.z : w.w, fb[j]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < MB; i++) {
+                            const uint4 w = x.a[i][2 * half + s / 2];
+                            const v8bf av = s % 2 ? cvt8_bf16(w.z, w.w, fa[i]) : cvt8_bf16(w.x, w.y, fa[i]);
+#pragma unroll
+                            for (int j = 0; j < NB; j++)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av, acc[i][j], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+        };
+        if (wave < units) {
+            NarrowUnit<A8, MB, NB> x;
+            load(wave, x);
+            int u = wave;
+            for (; u + W < units; u += W) {
+                NarrowUnit<A8, MB, NB> next;
+                load(u + W, next);
+                product(u, x);
+                x = next;
+            }
+            product(u, x);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; i++)
+#pragma unroll
+            for (int j = 0; j < NB; j++)
+                part[wave][i * NB + j][lane] = acc[i][j];
+        __syncthreads();
+        // register t of lane l: column (l / 16) * 4 + t, row l % 16 of a 16 x 16 block
+        for (int o = threadIdx.x; o < MB * NB * 64; o += W * 64) {
+            const int blk = o >> 6, l = o & 63;
+            v4f sum = part[0][blk][l];
+#pragma unroll
+            for (int w = 1; w < W; w++)
+                sum += part[w][blk][l];
+            const int64_t m = m0 + (blk / NB) * 16 + (l & 15), n = n0 + (blk % NB) * 16 + (l >> 4) * 4;
+            if (m < hi) {
+                const int64_t at = m * p.ldd + n;
+#pragma unroll
+                for (int t = 0; t < 4; t++)
+                    if (n + t < p.N) {
+                        if constexpr (OUT_BF16)
+                            ((__bf16 *)p.d)[at + t] = (__bf16)sum[t];
+                        else
+                            ((float *)p.d)[at + t] = p.accumulate ? ((float *)p.d)[at + t] + sum[t] : sum[t];
+                    }
             }
         }
+        __syncthreads();
     }
+}
+
+template <bool A8, int MB, int NB, int W> static void launch_narrow(const Mx4Args &p, bool bf16, hipStream_t st)
+{
+    const int tiles_n = (int)((p.N + 16 * NB - 1) / (16 * NB));
+    const int64_t all = (p.M + 16 * MB - 1) / (16 * MB);
+    const int chunks = p.offs ? 1 : (int)(all < 64 ? all : 64); // (experts' rows: a workgroup takes all)
+    const int64_t grid = (int64_t)((tiles_n + 7) / 8) * 8 * chunks * p.G;
+    if (bf16)
+        mx4_narrow_kernel<A8, MB, NB, W, true><<<(unsigned)grid, W * 64, 0, st>>>(p, tiles_n, chunks);
+    else
+        mx4_narrow_kernel<A8, MB, NB, W, false><<<(unsigned)grid, W * 64, 0, st>>>(p, tiles_n, chunks);
+}
+
+// The narrow kernel's tile: the largest of (16 MB rows, 16 NB columns) whose rows are
+// needed and whose workgroups still reach three quarters of the 256 CUs.  For one row
+// of 2048x7168, 28672x8192: (1, 1) 5.9, 32 us, (1, 4) 12, 29 us; 64 rows: (1, 2) 8.8,
+// 91 us, (4, 4) 20, 46 us.
+template <bool A8> static void launch_narrow_for(const Mx4Args &p, int64_t blocks, bool bf16, hipStream_t st)
+{
+    auto fills = [&](int MB, int NB) {
+        return (p.N + 16 * NB - 1) / (16 * NB) * (p.offs ? p.G : (blocks + MB - 1) / MB) >= 192;
+    };
+    if (blocks > 2 && fills(4, 4))
+        launch_narrow<A8, 4, 4, 4>(p, bf16, st);
+    else if (blocks > 1 && fills(2, 4))
+        launch_narrow<A8, 2, 4, 4>(p, bf16, st);
+    else if (fills(1, 4))
+        launch_narrow<A8, 1, 4, 4>(p, bf16, st);
+    else if (fills(1, 2))
+        launch_narrow<A8, 1, 2, 8>(p, bf16, st);
+    else
+        launch_narrow<A8, 1, 1, 8>(p, bf16, st);
 }
 
 static int check_mx4(const char *name, int a_fmt, int64_t M, int64_t N, int64_t K, int d_dtype)
@@ -114,20 +276,36 @@ template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16
     return launch_out<MODE_FP4, AG_STEP32, BG_STEP32, GK, FMT_E2M1, FMT_E2M1>(bf16, p, tiles, st);
 }
 
+// Narrow or tiled, by what each was measured to take.  The tiled kernel runs its
+// tiles 256 at a time, each round 8 us and 1.25 us a 256-element step (1.9 us a
+// 128-element step with an E4M3 A); the narrow one reads the weights' line once per
+// 16-64 rows and reaches 0.65 (0.38) PFLOP/s, less only where it is bound by bytes and
+// far ahead.  Measured, narrow against tiled, MXFP4 A: 512x2048x7168 20 / 42 us,
+// 1024x2048x7168 38 / 42, 256x7168x2048 18.5 / 18.1, 64x28672x8192 46 / 53,
+// 128x28672x8192 84 / 53; E4M3 A: 1024x2048x7168 62 / 115, 256x7168x2048 28 / 38,
+// 512x7168x2048 53 / 39, 64x28672x8192 77 / 133, 256x28672x8192 255 / 134.
+static bool takes_narrow(const Mx4Args &p, int a_fmt)
+{
+    const bool a8 = a_fmt == FGB_E4M3;
+    const double tile_us = a8 ? 8.0 + (double)(p.K / 128) * 1.9 : 8.0 + (double)((p.K + 255) / 256) * 1.25;
+    const int64_t tiles = ((p.M + 255) / 256 + (p.offs ? p.G / 2 : 0)) * ((p.N + 255) / 256);
+    const double narrow_us = 2e-9 * (double)p.M * (double)p.N * (double)p.K / (a8 ? 0.38 : 0.65);
+    return narrow_us <= tile_us * (double)((tiles + 255) / 256);
+}
+
 static int launch_mx4(const char *name, const Mx4Args &p, int a_fmt, int d_dtype, hipStream_t st)
 {
-    if (p.offs ? p.M > 64 * p.G : p.M > 64)
-        return p.offs ? launch_tiled<GK_M>(p, a_fmt, d_dtype == FGB_BF16, st)
-                      : launch_tiled<GK_NONE>(p, a_fmt, d_dtype == FGB_BF16, st);
-    const int64_t gx = (p.N + 31) / 32, tiles = (p.M + 31) / 32;
-    const dim3 grid((unsigned)gx, (unsigned)(p.offs ? (tiles < 16 ? tiles : 16) : (tiles < 65535 ? tiles : 65535)),
-                    (unsigned)p.G);
+    const bool bf16 = d_dtype == FGB_BF16;
+    if (!takes_narrow(p, a_fmt))
+        return p.offs ? launch_tiled<GK_M>(p, a_fmt, bf16, st) : launch_tiled<GK_NONE>(p, a_fmt, bf16, st);
+    // 16-row blocks, per expert for a grouped product: half a padding to 16 off the
+    // average, since M_cap is a bound
+    const int64_t rows = p.offs ? p.M / p.G - 8 : p.M, blocks = rows > 16 ? (rows + 15) / 16 : 1;
+    FGB_REQUIRE((p.N / 16 + 8) * 64 * p.G < (1ll << 31), FGB_EINVAL, "%s: too many tiles", name);
     if (a_fmt == FGB_E4M3)
-        d_dtype == FGB_BF16 ? mx4_gemm_kernel<true, true><<<grid, 64, 0, st>>>(p)
-                            : mx4_gemm_kernel<true, false><<<grid, 64, 0, st>>>(p);
+        launch_narrow_for<true>(p, blocks, bf16, st);
     else
-        d_dtype == FGB_BF16 ? mx4_gemm_kernel<false, true><<<grid, 64, 0, st>>>(p)
-                            : mx4_gemm_kernel<false, false><<<grid, 64, 0, st>>>(p);
+        launch_narrow_for<false>(p, blocks, bf16, st);
     FGB_LAUNCHED(name);
     return FGB_OK;
 }

@@ -1041,14 +1041,15 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
         _need(workspace, f"{name}: workspace", dtype=torch.uint8, contiguous=True)
     dev = _check_dev(logits, token_mask, workspace)
     if workspace is None:
-        workspace = torch.empty(max(moe_router_workspace_size(T, E), 4), dtype=torch.uint8, device=dev)
+        need = _lib.moe_router_workspace_size(T, E)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     idx = torch.empty((T, topk), dtype=torch.int32, device=dev)
     weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
     counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef else None
     _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(token_mask), score, int(bool(renorm)), scale,
-          loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(workspace), workspace.numel(),
-          _stream(logits))
+          loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _stream(logits))
     return idx, weights, counts, loss
 
 

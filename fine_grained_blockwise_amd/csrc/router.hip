@@ -20,9 +20,13 @@
 // A renormed sigmoid weight is formed from exp(z - m) / (1 + exp(z)), m =
 // min(0, max z), so that logits far below zero do not divide zero by zero.
 //
-// A wave takes one token at a time: lane l holds experts l R .. l R + R - 1.  All
-// sums are fp32 in a fixed order (the last, over workgroups, in fp64): results do
-// not depend on timing.
+// L lanes (8, 16, 32 or 64) take a token, lane l of them experts l R .. l R + R - 1:
+// the smallest L with L R >= E at R = 4, at least topk (lane j ends with slot j), so
+// a wave of a 32-expert router handles eight tokens at once.  A choice is a maximum
+// over the L lanes; its logit is read back from the winning key, so nothing is
+// broadcast.  All sums are fp32 in a fixed order (the last, over workgroups, in
+// fp64): results do not depend on timing.  Launches and instruction issue bound it:
+// 16384 x 32 logits are 2 MB.
 #include "fgb_internal.h"
 
 namespace fgb {
@@ -34,14 +38,17 @@ struct RouterArgs {
     int64_t T, ldz;
     int E, k;
     const uint8_t *mask;
-    int renorm;
+    int renorm, vec, vecd; // vec, vecd: rows of z, dz are whole aligned vectors
     float scale, coef;
     int32_t *idx;
     float *w;
     int32_t *counts; // [E + 1]
     float *loss;     // or NULL
-    int32_t *pcnt;   // [blocks][E + 1]
-    float *psum;     // [blocks][E]
+    // workspace: parts of the loss [reducing workgroups], the ticket (8 bytes), then
+    double *lpart;
+    int32_t *ticket;
+    float *psum;   // [blocks][E]
+    int32_t *pcnt; // [blocks][E + 1]
     // backward
     const float *dw;
     const float *dloss;
@@ -49,300 +56,471 @@ struct RouterArgs {
     int64_t lddz;
 };
 
-template <bool BF16> __device__ __forceinline__ float load_logit(const void *z, int64_t at)
+// The lane's R logits of a token; vec: rows are whole aligned vectors of R.
+template <bool BF16, int R>
+__device__ __forceinline__ void load_logits(const RouterArgs &a, int64_t t, int e0, float (&z)[R])
 {
-    return BF16 ? __uint_as_float((uint32_t)((const uint16_t *)z)[at] << 16) : ((const float *)z)[at];
+    if (a.vec) {
+        if (e0 >= a.E) {
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                z[j] = NEG_INF;
+        } else if constexpr (BF16) {
+            uint32_t w[R / 2];
+            const uint16_t *p = (const uint16_t *)a.z + t * a.ldz + e0;
+#pragma unroll
+            for (int j = 0; j < R / 4; j++) {
+                const uint2 u = reinterpret_cast<const uint2 *>(p)[j];
+                w[2 * j] = u.x;
+                w[2 * j + 1] = u.y;
+            }
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                z[j] = j % 2 ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]);
+        } else {
+            const float *p = (const float *)a.z + t * a.ldz + e0;
+#pragma unroll
+            for (int j = 0; j < R / 4; j++) {
+                const float4 u = reinterpret_cast<const float4 *>(p)[j];
+                z[4 * j] = u.x;
+                z[4 * j + 1] = u.y;
+                z[4 * j + 2] = u.z;
+                z[4 * j + 3] = u.w;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < R; j++) {
+        const int e = e0 + j;
+        if (e >= a.E)
+            z[j] = NEG_INF;
+        else if constexpr (BF16)
+            z[j] = __uint_as_float((uint32_t)((const uint16_t *)a.z)[t * a.ldz + e] << 16);
+        else
+            z[j] = ((const float *)a.z)[t * a.ldz + e];
+    }
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// Sum and maximum over aligned groups of L lanes; every lane gets the result.  Rows of
+// 16 lanes are joined by swapping them between two copies (VALU, no LDS round trip).
+template <int L> __device__ __forceinline__ float group_sum(float v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v += __shfl_xor(v, d);
+#define FGB_ADD(CTRL) v += __uint_as_float(dpp<CTRL>(__float_as_uint(v)))
+    FGB_ADD(FGB_DPP_QUAD_XOR1);
+    FGB_ADD(FGB_DPP_QUAD_XOR2);
+    FGB_ADD(FGB_DPP_HALF_MIRROR);
+    if constexpr (L >= 16)
+        FGB_ADD(FGB_DPP_ROW_ROR8);
+#undef FGB_ADD
+    if constexpr (L >= 32) {
+        const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
+    if constexpr (L >= 64) {
+        const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
     return v;
 }
-__device__ __forceinline__ float wave_max(float v)
+template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v = fmaxf(v, __shfl_xor(v, d));
+    v = group_max_u32<(L < 16 ? L : 16)>(v);
+    if constexpr (L >= 32) {
+        const auto w = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = max(w[0], w[1]);
+    }
+    if constexpr (L >= 64) {
+        const auto w = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max(w[0], w[1]);
+    }
     return v;
 }
 
-// Order-preserving map of a logit to an unsigned key; 0 for -inf and NaN, which
-// are never chosen.  -0 and +0 are equal logits and get one key.
+// Orders a wave's LDS accesses before and after it (other lanes' among them).
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Order-preserving map of a logit to an unsigned key and back; 0 for -inf and NaN,
+// which are never chosen.  -0 and +0 are equal logits and get one key.
 __device__ __forceinline__ uint32_t logit_key(float z)
 {
     const uint32_t u = __float_as_uint(z == 0.0f ? 0.0f : z);
     const uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
     return z > NEG_INF ? key : 0u;
 }
-
-// Scores of a live token: s (and for sigmoid scores the stable numerators t of
-// the renormed weights), and 1 / sum for p.
-template <int SCORE, int R>
-__device__ __forceinline__ void scores(const float (&z)[R], float (&s)[R], float (&p)[R], float (&t)[R])
+__device__ __forceinline__ float key_logit(uint32_t key)
 {
-    float m = NEG_INF;
-#pragma unroll
-    for (int j = 0; j < R; j++) {
-        m = fmaxf(m, z[j]);
-    }
-    m = wave_max(m);
-    float sum = 0.0f;
-    if constexpr (SCORE == FGB_ROUTER_SOFTMAX) {
-#pragma unroll
-        for (int j = 0; j < R; j++) {
-            s[j] = expf(z[j] - m);
-            sum += s[j];
-        }
-        sum = wave_sum(sum);
-#pragma unroll
-        for (int j = 0; j < R; j++)
-            t[j] = p[j] = s[j] = s[j] / sum;
-    } else {
-        const float m0 = fminf(m, 0.0f);
-#pragma unroll
-        for (int j = 0; j < R; j++) {
-            // z <= 0: exp(z) / (1 + exp(z)); z > 0: 1 / (1 + exp(-z)).
-            const float a = expf(-fabsf(z[j])), d = 1.0f + a;
-            s[j] = (z[j] > 0.0f ? 1.0f : a) / d;
-            t[j] = z[j] > 0.0f ? s[j] : expf(z[j] - m0) / d;
-            sum += t[j];
-        }
-        sum = wave_sum(sum);
-#pragma unroll
-        for (int j = 0; j < R; j++)
-            p[j] = t[j] / sum;
-    }
+    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
 }
 
-template <bool BF16, int SCORE, int R>
+// What a token's scores are formed with: for softmax m = max z and inv = 1 / sum
+// exp(z - m), for sigmoid m = min(0, max z) and inv = 1 / sum t.
+struct Norm {
+    float m, inv;
+};
+
+// exp(z - m) (softmax: s before its division), or the sigmoid's numerator
+// t = exp(z - m) / (1 + exp(z)), in the form that neither over- nor underflows.
+template <int SCORE> __device__ __forceinline__ float numerator(float z, float m)
+{
+    if constexpr (SCORE == FGB_ROUTER_SOFTMAX)
+        return expf(z - m);
+    const float d = 1.0f + expf(-fabsf(z));
+    return z > 0.0f ? 1.0f / d : expf(z - m) / d;
+}
+// sigmoid(z) itself (a weight without renorm).
+__device__ __forceinline__ float sigmoid(float z)
+{
+    const float a = expf(-fabsf(z));
+    return (z > 0.0f ? 1.0f : a) / (1.0f + a);
+}
+
+// The loss from sum_e counts_e sum_t p_te.
+__device__ __forceinline__ void write_loss(const RouterArgs &a, double sum, int live_n)
+{
+    const double n = live_n > 0 ? live_n : 1;
+    *a.loss = (float)((double)a.coef * a.E / (a.k * n * n) * sum);
+}
+
+// p of the lane's experts (num: the numerators), top the group's largest key.
+template <int SCORE, int L, int R>
+__device__ __forceinline__ Norm probabilities(const float (&z)[R], uint32_t top, float (&num)[R], float (&p)[R])
+{
+    Norm n;
+    n.m = key_logit(top);
+    if constexpr (SCORE == FGB_ROUTER_SIGMOID)
+        n.m = fminf(n.m, 0.0f);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < R; j++) {
+        num[j] = numerator<SCORE>(z[j], n.m);
+        sum += num[j];
+    }
+    n.inv = 1.0f / group_sum<L>(sum);
+#pragma unroll
+    for (int j = 0; j < R; j++)
+        p[j] = num[j] * n.inv;
+    return n;
+}
+
+template <bool BF16, int SCORE, int L, int R>
 __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
 {
-    extern __shared__ float red[]; // [4][E] floats, then [4][E + 1] ints
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    extern __shared__ float red[]; // [groups][E] floats (the loss's sums), then E + 1 ints
+    constexpr int GROUPS = 256 / L;
+    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = l * R;
+    int *cnt = reinterpret_cast<int *>(red + (a.loss ? GROUPS * a.E : 0));
+    for (int e = threadIdx.x; e <= a.E; e += 256)
+        cnt[e] = 0;
+    __syncthreads();
     float psum[R];
-    int cnt[R];
     int live_n = 0;
 #pragma unroll
-    for (int j = 0; j < R; j++) {
+    for (int j = 0; j < R; j++)
         psum[j] = 0.0f;
-        cnt[j] = 0;
-    }
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t t = t0 + group;
+        const bool on = t < a.T && (!a.mask || a.mask[t] != 0);
         float z[R];
-        uint32_t key[R];
-        uint32_t any = 0;
-        const bool on = !a.mask || a.mask[t] != 0;
+        uint32_t key[R], best = 0;
+        if (t < a.T) {
+            load_logits<BF16, R>(a, t, e0, z);
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                z[j] = NEG_INF;
+        }
 #pragma unroll
         for (int j = 0; j < R; j++) {
-            const int e = lane * R + j;
-            z[j] = e < a.E ? load_logit<BF16>(a.z, t * a.ldz + e) : NEG_INF;
-            key[j] = logit_key(z[j]);
-            any |= key[j];
+            key[j] = on ? logit_key(z[j]) : 0u;
+            best = max(best, key[j]);
         }
-        const bool live = on && __ballot(any != 0) != 0;
-        if (!live) { // uniform
-            if (lane < a.k) {
-                a.idx[t * a.k + lane] = -1;
-                a.w[t * a.k + lane] = 0.0f;
-            }
-            continue;
-        }
-        live_n++;
-        float s[R], p[R], num[R];
-        scores<SCORE, R>(z, s, p, num);
-#pragma unroll
-        for (int j = 0; j < R; j++)
-            psum[j] += p[j];
-        // top-k: the largest key over the wave, lowest lane and position first
-        float mine = 0.0f, total = 0.0f;
+        uint32_t top = group_max<L>(best);
+        const uint32_t first = top; // 0: the token is not live
+        // topk rounds; lane r keeps the r-th choice's logit and id
+        uint32_t mine = 0;
         int mine_e = -1;
         for (int r = 0; r < a.k; r++) {
-            uint32_t best = 0;
+            // the lowest lane with the largest key, its lowest position
+            const uint64_t hits = __ballot(best == top && top != 0);
+            const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
+                                    : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
+                                                    (L == 32 ? 0x80000000u : 1u << (L & 31)));
+            const bool won = l == win && best == top && top != 0;
             int at = 0;
+            uint32_t rest = 0;
+            bool look = won;
 #pragma unroll
-            for (int j = 0; j < R; j++)
-                if (key[j] > best) {
-                    best = key[j];
-                    at = j;
-                }
-            const uint32_t top = group_max_u32<64>(best);
-            if (top == 0)
-                break; // uniform: nothing left to choose
-            const int win = (int)__builtin_ctzll(__ballot(best == top));
-            float val = 0.0f;
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                if (j == at) {
-                    val = a.renorm ? num[j] : s[j];
-                    if (lane == win) {
-                        key[j] = 0;
-                        cnt[j]++;
-                    }
-                }
-            const float v = __shfl(val, win);
-            const int e = __shfl(lane * R + at, win);
-            total += v;
-            if (lane == r) {
-                mine = v;
+            for (int j = 0; j < R; j++) {
+                const bool hit = look && key[j] == top;
+                at = hit ? j : at;
+                key[j] = hit ? 0u : key[j];
+                look = look && !hit;
+                rest = max(rest, key[j]);
+            }
+            if (won)
+                atomicAdd(&cnt[e0 + at], 1); // integers: any order gives the same counts
+            // every lane of the group learns the id: one lane holds it, the others 0
+            const int e = (int)group_max<L>(won ? (uint32_t)(e0 + at + 1) : 0u) - 1;
+            if (l == r) {
+                mine = top;
                 mine_e = e;
             }
+            best = rest;
+            top = group_max<L>(best);
         }
-        if (lane < a.k) {
-            a.idx[t * a.k + lane] = mine_e;
-            a.w[t * a.k + lane] = mine_e < 0 ? 0.0f : a.scale * (a.renorm ? mine / total : mine);
+        float num[R], p[R];
+        const Norm n = probabilities<SCORE, L, R>(z, first, num, p);
+        // lane r: the weight of slot r
+        const float zr = key_logit(mine);
+        const float nr = mine ? numerator<SCORE>(zr, n.m) : 0.0f;
+        float w = nr * n.inv;
+        if (a.renorm) {
+            w = nr / group_sum<L>(nr);
+            // (a NaN logit is not chosen, but must not go unseen either)
+            w = n.inv == n.inv ? w : n.inv;
+        } else if (SCORE == FGB_ROUTER_SIGMOID) {
+            w = sigmoid(zr);
         }
-    }
-    // the workgroup's counts and sums, waves in order
-    float *fs = red;
-    int *is = reinterpret_cast<int *>(red + 4 * a.E);
+        if (t < a.T && l < a.k) {
+            a.idx[t * a.k + l] = mine_e;
+            a.w[t * a.k + l] = mine_e < 0 ? 0.0f : a.scale * w;
+        }
+        if (first != 0) {
+            live_n++;
 #pragma unroll
-    for (int j = 0; j < R; j++) {
-        const int e = lane * R + j;
-        if (e < a.E) {
-            fs[wave * a.E + e] = psum[j];
-            is[wave * (a.E + 1) + e] = cnt[j];
+            for (int j = 0; j < R; j++)
+                psum[j] += p[j];
         }
     }
-    if (lane == 0)
-        is[wave * (a.E + 1) + a.E] = live_n;
+    if (l == 0)
+        atomicAdd(&cnt[a.E], live_n);
+    if (a.loss) {
+#pragma unroll
+        for (int j = 0; j < R; j++)
+            if (e0 + j < a.E)
+                red[group * a.E + e0 + j] = psum[j];
+    }
     __syncthreads();
+    // the workgroup's counts and sums, groups in order; a lone workgroup finishes
+    const bool lone = gridDim.x == 1;
+    if (!lone && a.loss && blockIdx.x == 0 && threadIdx.x == 0)
+        *a.ticket = 0;
+    double part = 0.0;
     for (int e = threadIdx.x; e <= a.E; e += 256) {
-        int c = 0;
-        for (int w = 0; w < 4; w++)
-            c += is[w * (a.E + 1) + e];
-        a.pcnt[(int64_t)blockIdx.x * (a.E + 1) + e] = c;
-        if (e < a.E) {
-            float f = 0.0f;
-            for (int w = 0; w < 4; w++)
-                f += fs[w * a.E + e];
-            a.psum[(int64_t)blockIdx.x * a.E + e] = f;
-        }
-    }
-}
-
-// One workgroup: counts over the workgroups' partial results, and the loss.
-__global__ __launch_bounds__(256) void router_reduce_kernel(RouterArgs a, int blocks)
-{
-    __shared__ double part[256];
-    __shared__ int live_n;
-    double acc = 0.0;
-    for (int e = threadIdx.x; e <= a.E; e += 256) {
-        int c = 0;
-        double f = 0.0;
-        for (int b = 0; b < blocks; b++) {
-            c += a.pcnt[(int64_t)b * (a.E + 1) + e];
-            if (e < a.E)
-                f += a.psum[(int64_t)b * a.E + e];
-        }
-        a.counts[e] = c;
-        if (e == a.E)
-            live_n = c;
+        const int c = cnt[e];
+        if (lone)
+            a.counts[e] = c;
         else
-            acc += (double)c * f;
+            a.pcnt[(int64_t)blockIdx.x * (a.E + 1) + e] = c;
+        if (a.loss && e < a.E) {
+            float f = 0.0f;
+            for (int g = 0; g < GROUPS; g++)
+                f += red[g * a.E + e];
+            if (!lone)
+                a.psum[(int64_t)blockIdx.x * a.E + e] = f;
+            part += (double)c * f;
+        }
     }
-    part[threadIdx.x] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0 && a.loss) {
-        double sum = 0.0;
-        for (int i = 0; i < 256; i++)
-            sum += part[i];
-        const double n = live_n > 0 ? live_n : 1;
-        *a.loss = (float)((double)a.coef * a.E / (a.k * n * n) * sum);
+    if (lone && a.loss) {
+        __shared__ double parts[256];
+        parts[threadIdx.x] = part;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double sum = 0.0;
+            for (int i = 0; i < 256 && i < a.E; i++)
+                sum += parts[i];
+            write_loss(a, sum, cnt[a.E]);
+        }
     }
 }
 
-template <bool BF16, int SCORE, int R>
+// Counts and loss from the workgroups' partial results: 32 experts a workgroup, 32
+// threads to an expert, added in order.  The workgroup that comes last (the ticket,
+// zeroed by the forward kernel) adds the workgroups' parts of the loss, in order too.
+// One workgroup for all experts moved its 1 MB (512 partial results of 257 experts) at
+// one CU's rate: 60 us.
+constexpr int RED_COLS = 32, RED_SLICES = 32;
+__global__ __launch_bounds__(RED_COLS * RED_SLICES) void router_reduce_kernel(RouterArgs a, int blocks)
+{
+    __shared__ double fsum[RED_SLICES][RED_COLS];
+    __shared__ int csum[RED_SLICES][RED_COLS];
+    const int col = threadIdx.x % RED_COLS, slice = threadIdx.x / RED_COLS;
+    const int e = blockIdx.x * RED_COLS + col;
+    int c = 0;
+    double f = 0.0;
+    if (e <= a.E) {
+#pragma unroll 4
+        for (int b = slice; b < blocks; b += RED_SLICES)
+            c += a.pcnt[(int64_t)b * (a.E + 1) + e];
+    }
+    if (a.loss && e < a.E) {
+#pragma unroll 4
+        for (int b = slice; b < blocks; b += RED_SLICES)
+            f += a.psum[(int64_t)b * a.E + e];
+    }
+    csum[slice][col] = c;
+    fsum[slice][col] = f;
+    __syncthreads();
+    if (slice == 0) {
+        c = 0;
+        f = 0.0;
+        for (int s = 0; s < RED_SLICES; s++) {
+            c += csum[s][col];
+            f += fsum[s][col];
+        }
+        if (e <= a.E)
+            a.counts[e] = c;
+        fsum[0][col] = e < a.E ? (double)c * f : 0.0;
+    }
+    if (!a.loss)
+        return;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double sum = 0.0;
+        for (int i = 0; i < RED_COLS; i++)
+            sum += fsum[0][i];
+        a.lpart[blockIdx.x] = sum;
+        __threadfence(); // this workgroup's count of live tokens and part, before the ticket
+        if (atomicAdd(a.ticket, 1) == (int)gridDim.x - 1) {
+            __threadfence();
+            double parts = 0.0;
+            for (int i = 0; i < (int)gridDim.x; i++)
+                parts += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            write_loss(a, parts, __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        }
+    }
+}
+
+template <bool BF16, int SCORE, int L, int R>
 __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    extern __shared__ float lds[]; // [groups][L R]: D of the chosen experts
+    constexpr int GROUPS = 256 / L;
+    constexpr uint32_t NOT_CHOSEN = 0xFFFFFFFFu; // a NaN that D is never left as
+    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = l * R;
+    uint32_t *mine = reinterpret_cast<uint32_t *>(lds) + group * (L * R);
     const int n = a.counts[a.E];
     const float dl = a.dloss ? *a.dloss : 0.0f;
     const float f = n > 0 ? (float)((double)dl * a.coef * a.E / ((double)a.k * n * n)) : 0.0f;
     float g[R];
 #pragma unroll
-    for (int j = 0; j < R; j++) {
-        const int e = lane * R + j;
-        g[j] = e < a.E ? f * (float)a.counts[e] : 0.0f;
-    }
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
-        const int slot = lane < a.k ? a.idx[t * a.k + lane] : -1;
-        float dz[R];
+    for (int j = 0; j < R; j++)
+        g[j] = e0 + j < a.E ? f * (float)a.counts[e0 + j] : 0.0f;
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t t = t0 + group;
+        const int slot = t < a.T && l < a.k ? a.idx[t * a.k + l] : -1;
+        float z[R];
+        if (t < a.T) {
+            load_logits<BF16, R>(a, t, e0, z);
+        } else {
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                z[j] = NEG_INF;
+        }
+        float D = slot >= 0 && a.dw ? a.scale * a.dw[t * a.k + l] : 0.0f;
+        D = D == D ? D : __builtin_nanf("");
+        // to the lanes of the chosen experts, through LDS (one wave's accesses are in order)
 #pragma unroll
         for (int j = 0; j < R; j++)
-            dz[j] = 0.0f;
-        if (__ballot(slot >= 0) != 0) { // the token was live
-            float z[R], s[R], p[R], num[R];
+            mine[e0 + j] = NOT_CHOSEN;
+        wave_sync();
+        if (slot >= 0 && slot < a.E)
+            mine[slot] = __float_as_uint(D);
+        wave_sync();
+        float d[R];
+        bool on[R];
+        uint32_t best = 0;
 #pragma unroll
-            for (int j = 0; j < R; j++) {
-                const int e = lane * R + j;
-                z[j] = e < a.E ? load_logit<BF16>(a.z, t * a.ldz + e) : NEG_INF;
-            }
-            scores<SCORE, R>(z, s, p, num);
-            const float D = slot >= 0 && a.dw ? a.scale * a.dw[t * a.k + lane] : 0.0f;
-            // the chosen experts' scores: slot r's D at its expert
-            float d[R];
-            bool on[R];
+        for (int j = 0; j < R; j++) {
+            const uint32_t u = mine[e0 + j];
+            on[j] = u != NOT_CHOSEN;
+            d[j] = on[j] ? __uint_as_float(u) : 0.0f;
+            best = max(best, logit_key(z[j]));
+        }
+        const bool live = group_max<L>(slot >= 0 ? 1u : 0u) != 0;
+        float num[R], p[R], dz[R];
+        probabilities<SCORE, L, R>(z, group_max<L>(best), num, p);
+        float gp = 0.0f, chosen = 0.0f, dv = 0.0f, v[R];
 #pragma unroll
-            for (int j = 0; j < R; j++) {
-                d[j] = 0.0f;
-                on[j] = false;
-            }
-            for (int r = 0; r < a.k; r++) {
-                const int e = __shfl(slot, r);
-                const float Dr = __shfl(D, r);
-#pragma unroll
-                for (int j = 0; j < R; j++)
-                    if (e == lane * R + j) {
-                        d[j] = Dr;
-                        on[j] = true;
-                    }
-            }
-            float gp = 0.0f, chosen = 0.0f, dv = 0.0f;
-#pragma unroll
-            for (int j = 0; j < R; j++) {
-                gp += g[j] * p[j];
-                const float v = on[j] ? (a.renorm ? num[j] : s[j]) : 0.0f;
-                chosen += v;
-                dv += d[j] * v;
-            }
-            gp = wave_sum(gp);
-            chosen = wave_sum(chosen);
-            dv = wave_sum(dv);
-            const float mean = a.renorm ? dv / chosen : 0.0f;
-#pragma unroll
-            for (int j = 0; j < R; j++) {
-                const float v = !on[j] ? 0.0f : a.renorm ? num[j] / chosen : s[j];
-                float w = v * (d[j] - mean);
-                float l = p[j] * (g[j] - gp);
-                if constexpr (SCORE == FGB_ROUTER_SOFTMAX) {
-                    if (!a.renorm)
-                        l -= p[j] * dv;
-                } else {
-                    const float slope = 1.0f / (1.0f + expf(z[j])); // 1 - s, without cancellation
-                    w *= slope;
-                    l *= slope;
-                }
-                dz[j] = on[j] ? l + w : l;
-            }
+        for (int j = 0; j < R; j++) {
+            gp += g[j] * p[j];
+            v[j] = !on[j] ? 0.0f : a.renorm ? num[j] : SCORE == FGB_ROUTER_SIGMOID ? sigmoid(z[j]) : p[j];
+            chosen += v[j];
+            dv += d[j] * v[j];
+        }
+        gp = group_sum<L>(gp);
+        dv = group_sum<L>(dv);
+        float mean = 0.0f, inv = 1.0f;
+        if (a.renorm) {
+            inv = 1.0f / group_sum<L>(chosen);
+            mean = dv * inv;
         }
 #pragma unroll
         for (int j = 0; j < R; j++) {
-            const int e = lane * R + j;
-            if (e < a.E) {
-                if constexpr (BF16)
-                    ((__bf16 *)a.dz)[t * a.lddz + e] = (__bf16)dz[j];
-                else
-                    ((float *)a.dz)[t * a.lddz + e] = dz[j];
+            float w = v[j] * inv * (d[j] - mean);
+            float q = p[j] * (g[j] - gp);
+            if constexpr (SCORE == FGB_ROUTER_SOFTMAX) {
+                if (!a.renorm)
+                    q -= p[j] * dv;
+            } else {
+                const float one_minus = sigmoid(-z[j]); // 1 - s
+                w *= one_minus;
+                q *= one_minus;
             }
+            dz[j] = !live ? 0.0f : on[j] ? q + w : q;
+        }
+        if (t < a.T && a.vecd) {
+            if (e0 < a.E) {
+#pragma unroll
+                for (int j = 0; j < R; j += 4) {
+                    if constexpr (BF16)
+                        *reinterpret_cast<uint2 *>((uint16_t *)a.dz + t * a.lddz + e0 + j) =
+                            make_uint2(pack_bf16x2(dz[j], dz[j + 1]), pack_bf16x2(dz[j + 2], dz[j + 3]));
+                    else
+                        *reinterpret_cast<float4 *>((float *)a.dz + t * a.lddz + e0 + j) =
+                            make_float4(dz[j], dz[j + 1], dz[j + 2], dz[j + 3]);
+                }
+            }
+        } else if (t < a.T) {
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                if (e0 + j < a.E) {
+                    if constexpr (BF16)
+                        ((__bf16 *)a.dz)[t * a.lddz + e0 + j] = (__bf16)dz[j];
+                    else
+                        ((float *)a.dz)[t * a.lddz + e0 + j] = dz[j];
+                }
         }
     }
 }
 
-// Workgroups of the forward pass: four tokens each and pass, at most two per CU.
-static int64_t router_blocks(int64_t T) { return T < 4 ? 1 : T < 2048 ? (T + 3) / 4 : 512; }
+// Lanes per token.  Forward: a round of the choice costs about 4 R + 35 instructions
+// for 64 / L tokens, so fewer lanes with more experts each are faster (16384 x 256 with
+// the loss: 64 lanes of 4 40 us, 16 of 16 26 us).  Backward: memory and LDS accesses
+// of neighbouring lanes should be neighbours (16384 x 256: 17 us and 38 us).
+static int router_lanes(int E) { return E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64; }
+static int router_lanes_bwd(int E) { return E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
+// ... with lane j taking slot j.
+static int at_least_slots(int L, int k)
+{
+    const int need = k <= 8 ? 8 : k <= 16 ? 16 : k <= 32 ? 32 : 64;
+    return L > need ? L : need;
+}
+static int router_per_lane(int E, int L) { return 4 * L >= E ? 4 : 8 * L >= E && (L == 8 || L == 64) ? 8 : 16; }
+
+// Workgroups of the forward pass, at most four per CU; one alone needs no second launch.
+static int64_t router_blocks(int64_t T, int E)
+{
+    const int64_t per = 256 / router_lanes(E), n = (T + per - 1) / per;
+    return n < 1 ? 1 : n < 1024 ? n : 1024;
+}
+
+static int reduce_blocks(int E) { return (E + RED_COLS) / RED_COLS; }
 
 static int check_router(const char *name, const void *z, int dtype, int64_t T, int E, int64_t ldz, int k, int score)
 {
@@ -358,36 +536,44 @@ static int check_router(const char *name, const void *z, int dtype, int64_t T, i
     return FGB_OK;
 }
 
-template <bool BF16, int SCORE, bool FWD> static void launch_router(const RouterArgs &a, int64_t grid, hipStream_t st)
+template <bool BF16, int SCORE, bool FWD> static void launch_router(RouterArgs a, hipStream_t st)
 {
-    const size_t lds = FWD ? (size_t)4 * (2 * a.E + 1) * 4 : 0;
-#define FGB_R(N)                                                                                                       \
-    if constexpr (FWD)                                                                                                 \
-        router_fwd_kernel<BF16, SCORE, N><<<(unsigned)grid, 256, lds, st>>>(a);                                        \
-    else                                                                                                               \
-        router_bwd_kernel<BF16, SCORE, N><<<(unsigned)grid, 256, lds, st>>>(a);
-    if (a.E <= 64) {
-        FGB_R(1)
-    } else if (a.E <= 128) {
-        FGB_R(2)
-    } else if (a.E <= 256) {
-        FGB_R(4)
-    } else if (a.E <= 512) {
-        FGB_R(8)
-    } else {
-        FGB_R(16)
+    const int L = at_least_slots(FWD ? router_lanes(a.E) : router_lanes_bwd(a.E), a.k), groups = 256 / L;
+    const int R = router_per_lane(a.E, L);
+    a.vec = a.E % R == 0 && a.ldz % 4 == 0 && ((uintptr_t)a.z & (BF16 ? 7 : 15)) == 0;
+    a.vecd = a.E % R == 0 && a.lddz % 4 == 0 && ((uintptr_t)a.dz & (BF16 ? 7 : 15)) == 0;
+    const int64_t n = (a.T + groups - 1) / groups;
+    const unsigned grid = (unsigned)(FWD ? router_blocks(a.T, a.E) : n < 2048 ? n : 2048);
+    const size_t lds = FWD ? (size_t)4 * ((a.loss ? groups * a.E : 0) + a.E + 1) : (size_t)4 * 256 * R;
+#define FGB_R(LANES, PER)                                                                                              \
+    if (L == LANES && R == PER) {                                                                                      \
+        if constexpr (FWD)                                                                                             \
+            router_fwd_kernel<BF16, SCORE, LANES, PER><<<grid, 256, lds, st>>>(a);                                     \
+        else                                                                                                           \
+            router_bwd_kernel<BF16, SCORE, LANES, PER><<<grid, 256, lds, st>>>(a);                                     \
     }
+    FGB_R(8, 4)
+    FGB_R(8, 8)
+    FGB_R(8, 16)
+    FGB_R(16, 4)
+    FGB_R(16, 16)
+    FGB_R(32, 4)
+    FGB_R(32, 16)
+    FGB_R(64, 4)
+    FGB_R(64, 8)
+    FGB_R(64, 16)
 #undef FGB_R
 }
 
-template <bool FWD> static void dispatch_router(const RouterArgs &a, int dtype, int score, int64_t grid, hipStream_t st)
+template <bool FWD> static void dispatch_router(const RouterArgs &a, int dtype, int score, hipStream_t st)
 {
-    if (dtype == FGB_BF16)
-        score == FGB_ROUTER_SOFTMAX ? launch_router<true, FGB_ROUTER_SOFTMAX, FWD>(a, grid, st)
-                                    : launch_router<true, FGB_ROUTER_SIGMOID, FWD>(a, grid, st);
+    const bool bf16 = dtype == FGB_BF16;
+    if (bf16)
+        score == FGB_ROUTER_SOFTMAX ? launch_router<true, FGB_ROUTER_SOFTMAX, FWD>(a, st)
+                                    : launch_router<true, FGB_ROUTER_SIGMOID, FWD>(a, st);
     else
-        score == FGB_ROUTER_SOFTMAX ? launch_router<false, FGB_ROUTER_SOFTMAX, FWD>(a, grid, st)
-                                    : launch_router<false, FGB_ROUTER_SIGMOID, FWD>(a, grid, st);
+        score == FGB_ROUTER_SOFTMAX ? launch_router<false, FGB_ROUTER_SOFTMAX, FWD>(a, st)
+                                    : launch_router<false, FGB_ROUTER_SIGMOID, FWD>(a, st);
 }
 
 } // namespace fgb
@@ -398,7 +584,8 @@ extern "C" size_t moe_router_workspace_size(int64_t T, int E)
 {
     if (T < 0 || E < 1 || E > 1024)
         return 0;
-    return (size_t)router_blocks(T) * (2 * (size_t)E + 1) * 4;
+    const int64_t blocks = router_blocks(T, E);
+    return blocks == 1 ? 0 : (size_t)(reduce_blocks(E) + 1) * 8 + (size_t)blocks * (2 * (size_t)E + 1) * 4;
 }
 
 extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk,
@@ -413,20 +600,27 @@ extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64
     FGB_REQUIRE(counts && (T == 0 || (topk_idx && weights)), FGB_EINVAL, "moe_router: null pointer");
     FGB_REQUIRE((((uintptr_t)topk_idx | (uintptr_t)weights | (uintptr_t)counts | (uintptr_t)loss) & 3) == 0, FGB_EINVAL,
                 "moe_router: outputs must be 4-byte aligned");
-    FGB_REQUIRE(workspace && ws_bytes >= moe_router_workspace_size(T, E), FGB_EWORKSPACE,
-                "moe_router: workspace of %zu bytes needed", moe_router_workspace_size(T, E));
-    FGB_REQUIRE(((uintptr_t)workspace & 3) == 0, FGB_EINVAL, "moe_router: workspace must be 4-byte aligned");
-    const int64_t blocks = router_blocks(T);
+    const size_t need = moe_router_workspace_size(T, E);
+    FGB_REQUIRE(need == 0 || (workspace && ws_bytes >= need), FGB_EWORKSPACE, "moe_router: workspace of %zu bytes needed",
+                need);
+    FGB_REQUIRE(((uintptr_t)workspace & 7) == 0, FGB_EINVAL, "moe_router: workspace must be 8-byte aligned");
+    const int64_t blocks = router_blocks(T, E);
     RouterArgs a{};
     a.z = logits; a.T = T; a.ldz = ld; a.E = E; a.k = topk; a.mask = token_mask;
     a.renorm = renorm; a.scale = scale; a.coef = loss_coef;
     a.idx = topk_idx; a.w = weights; a.counts = counts; a.loss = loss;
-    a.psum = (float *)workspace;
-    a.pcnt = (int32_t *)((float *)workspace + blocks * E);
-    dispatch_router<true>(a, dtype, score, blocks, (hipStream_t)stream);
+    if (blocks > 1) {
+        a.lpart = (double *)workspace;
+        a.ticket = (int32_t *)(a.lpart + reduce_blocks(E));
+        a.psum = (float *)(a.lpart + reduce_blocks(E) + 1);
+        a.pcnt = (int32_t *)(a.psum + blocks * E);
+    }
+    dispatch_router<true>(a, dtype, score, (hipStream_t)stream);
     FGB_LAUNCHED("router_fwd_kernel");
-    router_reduce_kernel<<<1, 256, 0, (hipStream_t)stream>>>(a, (int)blocks);
-    FGB_LAUNCHED("router_reduce_kernel");
+    if (blocks > 1) {
+        router_reduce_kernel<<<reduce_blocks(E), RED_COLS * RED_SLICES, 0, (hipStream_t)stream>>>(a, (int)blocks);
+        FGB_LAUNCHED("router_reduce_kernel");
+    }
     return FGB_OK;
 }
 
@@ -451,7 +645,7 @@ extern "C" int moe_router_backward(const void *logits, int dtype, int64_t T, int
     a.renorm = renorm; a.scale = scale; a.coef = loss_coef;
     a.idx = (int32_t *)topk_idx; a.counts = (int32_t *)counts; a.dw = dweights; a.dloss = dloss;
     a.dz = dlogits; a.lddz = ldd;
-    dispatch_router<false>(a, dtype, score, T < 8192 ? (T + 3) / 4 : 2048, (hipStream_t)stream);
+    dispatch_router<false>(a, dtype, score, (hipStream_t)stream);
     FGB_LAUNCHED("router_bwd_kernel");
     return FGB_OK;
 }

@@ -672,8 +672,10 @@ int mxfp4_grouped_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uin
  *   counts[e]   = slots that chose e, counts[E] = the live tokens n
  *   loss        = loss_coef * E / (topk n^2) * sum_e counts[e] sum_t p[t][e] (0 if n = 0);
  *                 NULL: not computed
- *   A NaN or +inf logit of a live token makes its weights and the loss NaN.
- *   workspace: moe_router_workspace_size(T, E) bytes, contents on entry irrelevant.
+ *   A NaN logit of a live token (with softmax scores +inf too) makes NaN of what sums
+ *   over it: the loss, softmax and renormed weights, and the token's gradient.
+ *   workspace: moe_router_workspace_size(T, E) bytes (0 for a few tokens, then it may
+ *   be NULL), contents on entry irrelevant.
  * Sums are fp32 in a fixed order: results are the same on every run.
  */
 int moe_router(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk, const uint8_t *token_mask,

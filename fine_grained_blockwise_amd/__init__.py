@@ -145,11 +145,18 @@ def _ptr(t):
     # stream the temporary was allocated on, and torch's caching allocator only
     # hands a freed block to later work on that same stream, so the kernel
     # always reads it before anything can overwrite it.
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The handle of torch's current stream, without building a Stream object for it
+# (2 us a call, as much as half a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(t):
-    return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _dtype_code(t):
@@ -167,9 +174,10 @@ def _check_dev(*ts):
             continue
         if not t.is_cuda:
             raise ValueError("all tensors must be on the GPU")
+        d = t.device
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev = d
+        elif d != dev:
             raise ValueError("all tensors must be on the same GPU")
     return dev
 
@@ -186,7 +194,7 @@ def _need(t, name, shape=None, dtype=None, contiguous=False):
         raise ValueError(f"{name} is required")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(int(v) for v in shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(int(v) for v in shape):
         raise ValueError(f"{name} must have shape {tuple(int(v) for v in shape)}, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -902,33 +910,34 @@ def _mxfp4_shapes(rows, cols):
 
 
 def _mxfp4_input(x, name):
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise ValueError(f"{name}: x must be [rows, cols] or [G, rows, cols]")
     _dtype_code(x)
-    rows, cols = x.shape[-2:]
+    rows, cols = shape[-2:]
     if cols % 32:
         raise ValueError(f"{name}: cols ({cols}) must be a multiple of 32")
     _check_dev(x)
     # anything but aligned rows of unit stride (stacked without gaps) is copied once
-    ld = x.stride(-2)
-    if (x.stride(-1) != 1 or ld < cols or ld * x.element_size() % 16 or x.data_ptr() % 16
-            or (x.dim() == 3 and x.stride(0) != rows * ld)):
+    st = x.stride()
+    if (st[-1] != 1 or st[-2] < cols or st[-2] * x.element_size() % 16 or x.data_ptr() % 16
+            or (len(shape) == 3 and st[0] != rows * st[-2])):
         x = x.contiguous() if not x.is_contiguous() else x.clone()
-    return x
+    return x, tuple(shape[:-2]), rows, cols
 
 
-def _mxfp4_out(x, lead, rows, cols):
-    qs, ss = _mxfp4_shapes(rows, cols)
-    return [torch.empty(lead + shp, dtype=torch.uint8, device=x.device) for shp in (qs, ss)]
+def _mxfp4_out(lead, rows, cols, dev):
+    """Codes and scales of (stacked) MXFP4 tensors of rows x cols values."""
+    return (torch.empty(lead + (rows, cols // 2), dtype=torch.uint8, device=dev),
+            torch.empty(lead + ((cols + 255) // 256, rows, 8), dtype=torch.uint8, device=dev))
 
 
 def mxfp4_quant(x, rule=SCALE_CEIL):
     """MXFP4 quantization of x [rows, cols] (fp32/bf16, cols % 32 == 0) -> (q uint8 [rows, cols/2],
     s uint8 [ceil(cols/256), rows, 8]), or of stacked matrices x [G, rows, cols] -> (q [G, ...], s [G, ...]);
     see include/fgb.h for the layouts."""
-    x = _mxfp4_input(x, "mxfp4_quant")
-    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
-    q, s = _mxfp4_out(x, lead, rows, cols)
+    x, lead, rows, cols = _mxfp4_input(x, "mxfp4_quant")
+    q, s = _mxfp4_out(lead, rows, cols, x.device)
     _call("mxfp4_quant", _ptr(x), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule, _ptr(q),
           _ptr(s), _stream(x))
     return q, s
@@ -938,10 +947,9 @@ def mxfp4_quant_t(x, rule=SCALE_CEIL):
     """MXFP4 quantization of x [rows, cols] (or [G, rows, cols]) and of its transpose, in one pass:
     -> (q, s, qt, st), qt and st being those of a [cols, R] tensor, R = rows rounded up to 32 (columns past rows
     are zeros)."""
-    x = _mxfp4_input(x, "mxfp4_quant_t")
-    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
-    q, s = _mxfp4_out(x, lead, rows, cols)
-    qt, st = _mxfp4_out(x, lead, cols, (rows + 31) // 32 * 32)
+    x, lead, rows, cols = _mxfp4_input(x, "mxfp4_quant_t")
+    q, s = _mxfp4_out(lead, rows, cols, x.device)
+    qt, st = _mxfp4_out(lead, cols, (rows + 31) // 32 * 32, x.device)
     _call("mxfp4_quant_t", _ptr(x), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule, _ptr(q),
           _ptr(s), _ptr(qt), _ptr(st), _stream(x))
     return q, s, qt, st

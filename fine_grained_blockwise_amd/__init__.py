@@ -928,8 +928,8 @@ def _mxfp4_input(x, name):
 
 def _mxfp4_out(lead, rows, cols, dev):
     """Codes and scales of (stacked) MXFP4 tensors of rows x cols values."""
-    return (torch.empty(lead + (rows, cols // 2), dtype=torch.uint8, device=dev),
-            torch.empty(lead + ((cols + 255) // 256, rows, 8), dtype=torch.uint8, device=dev))
+    return (torch.empty(*lead, rows, cols // 2, dtype=torch.uint8, device=dev),
+            torch.empty(*lead, (cols + 255) // 256, rows, 8, dtype=torch.uint8, device=dev))
 
 
 def mxfp4_quant(x, rule=SCALE_CEIL):
@@ -963,7 +963,7 @@ def mxfp4_dequant(q, s, out_dtype=torch.float32):
     _need(q, "mxfp4_dequant: q", contiguous=True)
     _out_dtype(out_dtype, "mxfp4_dequant")
     _check_dev(q, s)
-    out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
+    out = torch.empty(rows, cols, dtype=out_dtype, device=q.device)
     _call("mxfp4_dequant", _ptr(q), _ptr(s), rows, cols, _ptr(out), _dtype_code(out), _stream(q))
     return out
 
@@ -992,7 +992,7 @@ def mxfp4_gemm(a, sa, b, sb, a_fmt=E2M1, out_dtype=torch.bfloat16, d=None, accum
     d = _gemm_out(d, M, N, out_dtype, name)
     _check_dev(a, sa, b, sb, d)
     if d is None:
-        d = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        d = torch.empty(M, N, dtype=out_dtype, device=a.device)
     _call(name, _ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), M, N, K, _row_ld(a), _row_ld(b), _ptr(d), _dtype_code(d),
           _row_ld(d), int(bool(accumulate)), _stream(a))
     return d
@@ -1013,7 +1013,7 @@ def mxfp4_grouped_gemm(a, sa, b, sb, group_offsets, a_fmt=E4M3, out_dtype=torch.
     d = _gemm_out(d, M_cap, N, out_dtype, name, contiguous=True)
     _check_dev(a, sa, b, sb, group_offsets, d)
     if d is None:
-        d = torch.empty((M_cap, N), dtype=out_dtype, device=a.device)
+        d = torch.empty(M_cap, N, dtype=out_dtype, device=a.device)
     _call(name, _ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), _ptr(group_offsets), G, M_cap, N, K, _ptr(d),
           _dtype_code(d), _stream(a))
     return d
@@ -1051,8 +1051,8 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
     if workspace is None:
         need = _lib.moe_router_workspace_size(T, E)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    idx = torch.empty((T, topk), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    idx = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
     counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef else None
     _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(token_mask), score, int(bool(renorm)), scale,
@@ -1079,7 +1079,7 @@ def moe_router_backward(logits, topk_idx, counts, dweights=None, dloss=None, sco
         if dloss.numel() != 1:
             raise ValueError(f"{name}: dloss must hold one value")
     _check_dev(logits, topk_idx, counts, dweights, dloss)
-    dz = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    dz = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
     _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(topk_idx), _ptr(counts), _ptr(dweights),
           _ptr(dloss), score, int(bool(renorm)), scale, loss_coef, _ptr(dz), E, _stream(logits))
     return dz

@@ -29,7 +29,8 @@ struct Mx4Args {
 // memory: lane l holds row l % 16 and the 32-element groups l / 16 and 4 + l / 16 of
 // a unit, so a load instruction covers 64 contiguous bytes of 16 rows, and a lane
 // ends with four consecutive columns of one row of D.  The next unit's loads are
-// issued before a unit is multiplied.
+// issued before a unit is multiplied.  One token's eight experts (4096x7168, E4M3 A,
+// 125 MB): 30 us, 4.2 TB/s; 28672x8192: 29 us, 4.3 TB/s with 4 us of launch in it.
 template <bool A8, int MB, int NB> struct NarrowUnit {
     uint4 b[NB][2], a[MB][A8 ? 4 : 2];
     uint2 bs[NB], as[MB]; // scale bytes of a row: all eight groups (an E4M3 A: .x holds its two)
@@ -37,16 +38,26 @@ template <bool A8, int MB, int NB> struct NarrowUnit {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+// A raw buffer descriptor of `bytes` bytes at a wave-uniform address.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *q, int64_t bytes)
+{
+    const uint64_t v = (uint64_t)(uintptr_t)q;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)(((uint64_t)hi << 32) | lo), 0,
+                                             __builtin_amdgcn_readfirstlane((int)bytes), BUF_DWORD3);
+}
+
 template <bool A8, int MB, int NB, int W, bool OUT_BF16>
 __global__ __launch_bounds__(W * 64) void mx4_narrow_kernel(Mx4Args p, int tiles_n, int chunks)
 {
     __shared__ v4f part[W][MB * NB][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, h = lane >> 4;
+    const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Workgroup -> (column tile, row chunk, expert): eight column tiles, then their
     // next chunk, so that the chunks of a column tile run on one XCD (b % 8) and
     // find its weights in that L2.
     const int64_t per = (int64_t)((tiles_n + 7) / 8) * 8 * chunks;
-    const int e = (int)(blockIdx.x / per);
+    int e = (int)(blockIdx.x / per);
     const int64_t in = blockIdx.x % per;
     const int tn = (int)(in / (8 * chunks)) * 8 + (int)(in & 7), chunk = (int)(in / 8 % chunks);
     if (tn >= tiles_n)
@@ -56,58 +67,78 @@ __global__ __launch_bounds__(W * 64) void mx4_narrow_kernel(Mx4Args p, int tiles
     const uint8_t *b = p.b, *sb = p.sb;
     const int units = (int)((p.K + 255) / 256), groups = (int)(p.K / 32);
     if (p.offs) {
-        lo = p.offs[e];
-        hi = p.offs[e + 1];
+        // the e-th expert that has rows: the workgroups with work come first
+        int want = e;
+        e = -1;
+        for (int g0 = 0; g0 < p.G && e < 0; g0 += 64) {
+            const int g = g0 + lane;
+            const int32_t o0 = g < p.G ? p.offs[g] : 0, o1 = g < p.G ? p.offs[g + 1] : 0;
+            const uint64_t live = __ballot(o1 > o0);
+            const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(live >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)live, 0));
+            const uint64_t hit = __ballot(o1 > o0 && rank == want);
+            if (hit) {
+                const int l = __builtin_ctzll(hit);
+                e = g0 + l;
+                lo = __builtin_amdgcn_readlane(o0, l);
+                hi = __builtin_amdgcn_readlane(o1, l);
+            }
+            want -= __builtin_popcountll(live);
+        }
+        if (e < 0)
+            return; // uniform over the workgroup
         b += (int64_t)e * p.N * p.ldb;
         sb += (int64_t)e * p.N * units * 8;
     }
-    const uint8_t *brow[NB], *bsrow[NB];
-#pragma unroll
-    for (int j = 0; j < NB; j++) {
-        const int64_t n = n0 + j * 16 + r < p.N ? n0 + j * 16 + r : p.N - 1;
-        brow[j] = b + n * p.ldb + h * 16;
-        bsrow[j] = sb + n * 8;
-    }
+    // Buffer loads: one offset register serves a lane's rows, and what lies past an
+    // operand's last row reads as zeros.
+    b += n0 * p.ldb;
+    sb += n0 * 8;
+    const int bn = (int)min((int64_t)(16 * NB), p.N - n0);
+    const auto brs = buffer(b, (bn - 1) * p.ldb + p.K / 2);
+    const uint32_t boff = (uint32_t)(r * p.ldb + h * 16);
     for (int64_t m0 = lo + (int64_t)chunk * (16 * MB); m0 < hi; m0 += (int64_t)chunks * (16 * MB)) {
-        const uint8_t *arow[MB], *asrow[MB];
-#pragma unroll
-        for (int i = 0; i < MB; i++) {
-            const int64_t m = m0 + i * 16 + r < hi ? m0 + i * 16 + r : hi - 1;
-            arow[i] = p.a + m * p.lda + h * (A8 ? 32 : 16);
-            asrow[i] = A8 ? p.sa + m * (p.K / 128) : p.sa + m * 8;
-        }
+        const int am = (int)min((int64_t)(16 * MB), hi - m0);
+        const auto ars = buffer(p.a + m0 * p.lda, (am - 1) * p.lda + (A8 ? p.K : p.K / 2));
+        const uint32_t aoff = (uint32_t)(r * p.lda + h * (A8 ? 32 : 16));
+        const int64_t as_row = p.K / 128; // E4M3 A: its scales, row-major
+        const auto asrs8 = buffer(p.sa + m0 * as_row, am * as_row);
         v4f acc[MB][NB];
 #pragma unroll
         for (int i = 0; i < MB; i++)
 #pragma unroll
             for (int j = 0; j < NB; j++)
                 acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-        // A group past K reads bytes of the row's first unit instead; product() then
-        // takes zeros for A (not here: nothing may wait for a load where it is issued).
+        // (What is read of groups past K is replaced in product(), not here: nothing
+        // may wait for a load where it is issued.)
         auto load = [&](int u, NarrowUnit<A8, MB, NB> &x) {
-            const bool in0 = u * 8 + h < groups, in1 = u * 8 + 4 + h < groups;
-            const int64_t u0 = in0 ? (int64_t)u * 128 : -(int64_t)h * 16, u1 = in1 ? (int64_t)u * 128 + 64 : -(int64_t)h * 16;
+            const auto bsrs = buffer(sb + (int64_t)u * p.N * 8, bn * 8);
 #pragma unroll
             for (int j = 0; j < NB; j++) {
-                x.b[j][0] = *reinterpret_cast<const uint4 *>(brow[j] + u0);
-                x.b[j][1] = *reinterpret_cast<const uint4 *>(brow[j] + u1);
-                x.bs[j] = *reinterpret_cast<const uint2 *>(bsrow[j] + (int64_t)u * p.N * 8);
+                const uint32_t at = (uint32_t)(j * 16 * p.ldb) + (uint32_t)u * 128;
+                x.b[j][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff, at, 0));
+                x.b[j][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff + 64, at, 0));
+                x.bs[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bsrs, r * 8 + j * 128, 0, 0));
             }
+            if constexpr (A8) {
 #pragma unroll
-            for (int i = 0; i < MB; i++) {
-                if constexpr (A8) {
-                    const uint4 *q0 = reinterpret_cast<const uint4 *>(arow[i] + 2 * u0);
-                    const uint4 *q1 = reinterpret_cast<const uint4 *>(arow[i] + 2 * u1);
-                    x.a[i][0] = q0[0];
-                    x.a[i][1] = q0[1];
-                    x.a[i][2] = q1[0];
-                    x.a[i][3] = q1[1];
-                    x.as[i].x = asrow[i][2 * u];
-                    x.as[i].y = asrow[i][in1 ? 2 * u + 1 : 2 * u];
-                } else {
-                    x.a[i][0] = *reinterpret_cast<const uint4 *>(arow[i] + u0);
-                    x.a[i][1] = *reinterpret_cast<const uint4 *>(arow[i] + u1);
-                    x.as[i] = *reinterpret_cast<const uint2 *>(asrow[i] + (int64_t)u * p.M * 8);
+                for (int i = 0; i < MB; i++) {
+                    const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 256;
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        x.a[i][k] = __builtin_bit_cast(
+                            uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + (k / 2) * 128 + (k & 1) * 16, at, 0));
+                    const uint32_t row = (uint32_t)((i * 16 + r) * as_row);
+                    x.as[i].x = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row, 2 * u, 0);
+                    x.as[i].y = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row + 1, 2 * u, 0);
+                }
+            } else {
+                const auto asrs = buffer(p.sa + ((int64_t)u * p.M + m0) * 8, am * 8);
+#pragma unroll
+                for (int i = 0; i < MB; i++) {
+                    const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 128;
+                    x.a[i][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff, at, 0));
+                    x.a[i][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + 64, at, 0));
+                    x.as[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(asrs, r * 8 + i * 128, 0, 0));
                 }
             }
         };
@@ -123,6 +154,8 @@ __global__ __launch_bounds__(W * 64) void mx4_narrow_kernel(Mx4Args p, int tiles
                             x.a[i][q] = make_uint4(0, 0, 0, 0);
                         if (!in1)
                             x.a[i][Q + q] = make_uint4(0, 0, 0, 0);
+                        if (A8 && !in1) // the byte after the row's last is another row's
+                            x.as[i].y = 0;
                     }
             }
             if constexpr (!A8) {
@@ -225,8 +258,8 @@ template <bool A8, int MB, int NB, int W> static void launch_narrow(const Mx4Arg
 
 // The narrow kernel's tile: the largest of (16 MB rows, 16 NB columns) whose rows are
 // needed and whose workgroups still reach three quarters of the 256 CUs.  For one row
-// of 2048x7168, 28672x8192: (1, 1) 5.9, 32 us, (1, 4) 12, 29 us; 64 rows: (1, 2) 8.8,
-// 91 us, (4, 4) 20, 46 us.
+// of 2048x7168, 28672x8192: (1, 1) 5.7, 32 us, (1, 4) 12, 29 us; 64 rows: (1, 2) 8.7,
+// 91 us, (4, 4) 20, 44 us.
 template <bool A8> static void launch_narrow_for(const Mx4Args &p, int64_t blocks, bool bf16, hipStream_t st)
 {
     auto fills = [&](int MB, int NB) {
@@ -278,16 +311,19 @@ template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16
 
 // Narrow or tiled, by what each was measured to take.  The tiled kernel runs its
 // tiles 256 at a time, each round 8 us and 1.25 us a 256-element step (1.9 us a
-// 128-element step with an E4M3 A); the narrow one reads the weights' line once per
-// 16-64 rows and reaches 0.65 (0.38) PFLOP/s, less only where it is bound by bytes and
-// far ahead.  Measured, narrow against tiled, MXFP4 A: 512x2048x7168 20 / 42 us,
-// 1024x2048x7168 38 / 42, 256x7168x2048 18.5 / 18.1, 64x28672x8192 46 / 53,
-// 128x28672x8192 84 / 53; E4M3 A: 1024x2048x7168 62 / 115, 256x7168x2048 28 / 38,
-// 512x7168x2048 53 / 39, 64x28672x8192 77 / 133, 256x28672x8192 255 / 134.
+// 128-element step with an E4M3 A), 1.4 times that where every tile reads other
+// weights (experts of few rows); the narrow one reads the weights once per 16-64 rows
+// and reaches 0.65 (0.38) PFLOP/s, less only where it is bound by bytes and far ahead.
+// Measured, narrow against tiled, MXFP4 A: 512x2048x7168 20 / 42 us, 1024x2048x7168
+// 38 / 42, 256x7168x2048 18.5 / 18.1, 64x28672x8192 44 / 53, 128x28672x8192 84 / 53, 32
+// experts of 16 rows (4096x7168) 106 / 122; E4M3 A: 1024x2048x7168 62 / 115,
+// 256x7168x2048 28 / 38, 512x7168x2048 53 / 39, 64x28672x8192 75 / 133, 256x28672x8192
+// 255 / 134, 32 experts of 48 rows 248 / 324.
 static bool takes_narrow(const Mx4Args &p, int a_fmt)
 {
     const bool a8 = a_fmt == FGB_E4M3;
-    const double tile_us = a8 ? 8.0 + (double)(p.K / 128) * 1.9 : 8.0 + (double)((p.K + 255) / 256) * 1.25;
+    const double step_us = a8 ? (double)(p.K / 128) * 1.9 : (double)((p.K + 255) / 256) * 1.25;
+    const double tile_us = (8.0 + step_us) * (p.offs ? 1.4 : 1.0);
     const int64_t tiles = ((p.M + 255) / 256 + (p.offs ? p.G / 2 : 0)) * ((p.N + 255) / 256);
     const double narrow_us = 2e-9 * (double)p.M * (double)p.N * (double)p.K / (a8 ? 0.38 : 0.65);
     return narrow_us <= tile_us * (double)((tiles + 255) / 256);

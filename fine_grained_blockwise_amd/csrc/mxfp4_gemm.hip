@@ -53,194 +53,199 @@ __global__ __launch_bounds__(W * 64) void mx4_narrow_kernel(Mx4Args p, int tiles
     __shared__ v4f part[W][MB * NB][64];
     const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // Workgroup -> (column tile, row chunk, expert): eight column tiles, then their
-    // next chunk, so that the chunks of a column tile run on one XCD (b % 8) and
-    // find its weights in that L2.
-    const int64_t per = (int64_t)((tiles_n + 7) / 8) * 8 * chunks;
-    int e = (int)(blockIdx.x / per);
-    const int64_t in = blockIdx.x % per;
-    const int tn = (int)(in / (8 * chunks)) * 8 + (int)(in & 7), chunk = (int)(in / 8 % chunks);
-    if (tn >= tiles_n)
-        return;
-    const int64_t n0 = (int64_t)tn * (16 * NB);
-    int64_t lo = 0, hi = p.M;
-    const uint8_t *b = p.b, *sb = p.sb;
     const int units = (int)((p.K + 255) / 256), groups = (int)(p.K / 32);
-    if (p.offs) {
-        // the e-th expert that has rows: the workgroups with work come first
-        int want = e;
-        e = -1;
-        for (int g0 = 0; g0 < p.G && e < 0; g0 += 64) {
-            const int g = g0 + lane;
-            const int32_t o0 = g < p.G ? p.offs[g] : 0, o1 = g < p.G ? p.offs[g + 1] : 0;
-            const uint64_t live = __ballot(o1 > o0);
-            const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(live >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)live, 0));
-            const uint64_t hit = __ballot(o1 > o0 && rank == want);
-            if (hit) {
-                const int l = __builtin_ctzll(hit);
-                e = g0 + l;
-                lo = __builtin_amdgcn_readlane(o0, l);
-                hi = __builtin_amdgcn_readlane(o1, l);
+    // Dense: workgroup -> (column tile, row chunk): eight column tiles, then their next
+    // chunk, so that the chunks of a column tile run on one XCD (b % 8) and find its
+    // weights in that L2.  Per expert: the (expert with rows, column tile) pairs in turn,
+    // by as many workgroups as run at once (8 busy experts of 32, 7168x2048: 22.6 us
+    // with a workgroup for every pair of the host's bound, 20.7 us so).
+    for (int64_t task = blockIdx.x;; task += gridDim.x) {
+        int tn, chunk = 0;
+        int64_t lo = 0, hi = p.M;
+        const uint8_t *b = p.b, *sb = p.sb;
+        if (!p.offs) {
+            tn = (int)(task / (8 * chunks)) * 8 + (int)(task & 7);
+            chunk = (int)(task / 8 % chunks);
+            if (tn >= tiles_n)
+                return;
+        } else {
+            tn = (int)(task % tiles_n);
+            int want = (int)(task / tiles_n), e = -1;
+            for (int g0 = 0; g0 < p.G && e < 0; g0 += 64) {
+                const int g = g0 + lane;
+                const int32_t o0 = g < p.G ? p.offs[g] : 0, o1 = g < p.G ? p.offs[g + 1] : 0;
+                const uint64_t live = __ballot(o1 > o0);
+                const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(live >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)live, 0));
+                const uint64_t hit = __ballot(o1 > o0 && rank == want);
+                if (hit) {
+                    const int l = __builtin_ctzll(hit);
+                    e = g0 + l;
+                    lo = __builtin_amdgcn_readlane(o0, l);
+                    hi = __builtin_amdgcn_readlane(o1, l);
+                }
+                want -= __builtin_popcountll(live);
             }
-            want -= __builtin_popcountll(live);
+            if (e < 0)
+                return; // uniform over the workgroup: no pair is left
+            b += (int64_t)e * p.N * p.ldb;
+            sb += (int64_t)e * p.N * units * 8;
         }
-        if (e < 0)
-            return; // uniform over the workgroup
-        b += (int64_t)e * p.N * p.ldb;
-        sb += (int64_t)e * p.N * units * 8;
-    }
-    // Buffer loads: one offset register serves a lane's rows, and what lies past an
-    // operand's last row reads as zeros.
-    b += n0 * p.ldb;
-    sb += n0 * 8;
-    const int bn = (int)min((int64_t)(16 * NB), p.N - n0);
-    const auto brs = buffer(b, (bn - 1) * p.ldb + p.K / 2);
-    const uint32_t boff = (uint32_t)(r * p.ldb + h * 16);
-    for (int64_t m0 = lo + (int64_t)chunk * (16 * MB); m0 < hi; m0 += (int64_t)chunks * (16 * MB)) {
-        const int am = (int)min((int64_t)(16 * MB), hi - m0);
-        const auto ars = buffer(p.a + m0 * p.lda, (am - 1) * p.lda + (A8 ? p.K : p.K / 2));
-        const uint32_t aoff = (uint32_t)(r * p.lda + h * (A8 ? 32 : 16));
-        const int64_t as_row = p.K / 128; // E4M3 A: its scales, row-major
-        const auto asrs8 = buffer(p.sa + m0 * as_row, am * as_row);
-        v4f acc[MB][NB];
+        const int64_t n0 = (int64_t)tn * (16 * NB);
+        // Buffer loads: one offset register serves a lane's rows, and what lies past an
+        // operand's last row reads as zeros.
+        b += n0 * p.ldb;
+        sb += n0 * 8;
+        const int bn = (int)min((int64_t)(16 * NB), p.N - n0);
+        const auto brs = buffer(b, (bn - 1) * p.ldb + p.K / 2);
+        const uint32_t boff = (uint32_t)(r * p.ldb + h * 16);
+        for (int64_t m0 = lo + (int64_t)chunk * (16 * MB); m0 < hi; m0 += (int64_t)chunks * (16 * MB)) {
+            const int am = (int)min((int64_t)(16 * MB), hi - m0);
+            const auto ars = buffer(p.a + m0 * p.lda, (am - 1) * p.lda + (A8 ? p.K : p.K / 2));
+            const uint32_t aoff = (uint32_t)(r * p.lda + h * (A8 ? 32 : 16));
+            const int64_t as_row = p.K / 128; // E4M3 A: its scales, row-major
+            const auto asrs8 = buffer(p.sa + m0 * as_row, am * as_row);
+            v4f acc[MB][NB];
 #pragma unroll
-        for (int i = 0; i < MB; i++)
+            for (int i = 0; i < MB; i++)
 #pragma unroll
-            for (int j = 0; j < NB; j++)
-                acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-        // (What is read of groups past K is replaced in product(), not here: nothing
-        // may wait for a load where it is issued.)
-        auto load = [&](int u, NarrowUnit<A8, MB, NB> &x) {
-            const auto bsrs = buffer(sb + (int64_t)u * p.N * 8, bn * 8);
+                for (int j = 0; j < NB; j++)
+                    acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+            // (What is read of groups past K is replaced in product(), not here: nothing
+            // may wait for a load where it is issued.)
+            auto load = [&](int u, NarrowUnit<A8, MB, NB> &x) {
+                const auto bsrs = buffer(sb + (int64_t)u * p.N * 8, bn * 8);
 #pragma unroll
-            for (int j = 0; j < NB; j++) {
-                const uint32_t at = (uint32_t)(j * 16 * p.ldb) + (uint32_t)u * 128;
-                x.b[j][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff, at, 0));
-                x.b[j][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff + 64, at, 0));
-                x.bs[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bsrs, r * 8 + j * 128, 0, 0));
-            }
-            if constexpr (A8) {
-#pragma unroll
-                for (int i = 0; i < MB; i++) {
-                    const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 256;
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        x.a[i][k] = __builtin_bit_cast(
-                            uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + (k / 2) * 128 + (k & 1) * 16, at, 0));
-                    const uint32_t row = (uint32_t)((i * 16 + r) * as_row);
-                    x.as[i].x = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row, 2 * u, 0);
-                    x.as[i].y = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row + 1, 2 * u, 0);
+                for (int j = 0; j < NB; j++) {
+                    const uint32_t at = (uint32_t)(j * 16 * p.ldb) + (uint32_t)u * 128;
+                    x.b[j][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff, at, 0));
+                    x.b[j][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff + 64, at, 0));
+                    x.bs[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bsrs, r * 8 + j * 128, 0, 0));
                 }
-            } else {
-                const auto asrs = buffer(p.sa + ((int64_t)u * p.M + m0) * 8, am * 8);
+                if constexpr (A8) {
 #pragma unroll
-                for (int i = 0; i < MB; i++) {
-                    const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 128;
-                    x.a[i][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff, at, 0));
-                    x.a[i][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + 64, at, 0));
-                    x.as[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(asrs, r * 8 + i * 128, 0, 0));
-                }
-            }
-        };
-        auto product = [&](int u, NarrowUnit<A8, MB, NB> &x) {
-            if (u * 8 + 8 > groups) { // uniform: the last unit of a K that is no multiple of 256
-                const bool in0 = u * 8 + h < groups, in1 = u * 8 + 4 + h < groups;
-                constexpr int Q = A8 ? 2 : 1;
+                    for (int i = 0; i < MB; i++) {
+                        const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 256;
 #pragma unroll
-                for (int i = 0; i < MB; i++)
-#pragma unroll
-                    for (int q = 0; q < Q; q++) {
-                        if (!in0)
-                            x.a[i][q] = make_uint4(0, 0, 0, 0);
-                        if (!in1)
-                            x.a[i][Q + q] = make_uint4(0, 0, 0, 0);
-                        if (A8 && !in1) // the byte after the row's last is another row's
-                            x.as[i].y = 0;
+                        for (int k = 0; k < 4; k++)
+                            x.a[i][k] = __builtin_bit_cast(
+                                uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + (k / 2) * 128 + (k & 1) * 16, at, 0));
+                        const uint32_t row = (uint32_t)((i * 16 + r) * as_row);
+                        x.as[i].x = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row, 2 * u, 0);
+                        x.as[i].y = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row + 1, 2 * u, 0);
                     }
-            }
-            if constexpr (!A8) {
+                } else {
+                    const auto asrs = buffer(p.sa + ((int64_t)u * p.M + m0) * 8, am * 8);
 #pragma unroll
-                for (int half = 0; half < 2; half++)
+                    for (int i = 0; i < MB; i++) {
+                        const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 128;
+                        x.a[i][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff, at, 0));
+                        x.a[i][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + 64, at, 0));
+                        x.as[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(asrs, r * 8 + i * 128, 0, 0));
+                    }
+                }
+            };
+            auto product = [&](int u, NarrowUnit<A8, MB, NB> &x) {
+                if (u * 8 + 8 > groups) { // uniform: the last unit of a K that is no multiple of 256
+                    const bool in0 = u * 8 + h < groups, in1 = u * 8 + 4 + h < groups;
+                    constexpr int Q = A8 ? 2 : 1;
 #pragma unroll
                     for (int i = 0; i < MB; i++)
 #pragma unroll
-                        for (int j = 0; j < NB; j++) {
-                            const uint4 bw = x.b[j][half], aw = x.a[i][half];
-                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                (v8i){(int)bw.x, (int)bw.y, (int)bw.z, (int)bw.w, 0, 0, 0, 0},
-                                (v8i){(int)aw.x, (int)aw.y, (int)aw.z, (int)aw.w, 0, 0, 0, 0}, acc[i][j], 4, 4, 0,
-                                (int)((half ? x.bs[j].y : x.bs[j].x) >> (8 * h)), 0,
-                                (int)((half ? x.as[i].y : x.as[i].x) >> (8 * h)));
+                        for (int q = 0; q < Q; q++) {
+                            if (!in0)
+                                x.a[i][q] = make_uint4(0, 0, 0, 0);
+                            if (!in1)
+                                x.a[i][Q + q] = make_uint4(0, 0, 0, 0);
+                            if (A8 && !in1) // the byte after the row's last is another row's
+                                x.as[i].y = 0;
                         }
-            } else {
+                }
+                if constexpr (!A8) {
 #pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    float fa[MB], fb[NB];
+                    for (int half = 0; half < 2; half++)
 #pragma unroll
-                    for (int i = 0; i < MB; i++)
-                        fa[i] = scale_f32(half ? x.as[i].y : x.as[i].x);
+                        for (int i = 0; i < MB; i++)
 #pragma unroll
-                    for (int j = 0; j < NB; j++)
-                        fb[j] = scale_f32(((half ? x.bs[j].y : x.bs[j].x) >> (8 * h)) & 0xFFu);
+                            for (int j = 0; j < NB; j++) {
+                                const uint4 bw = x.b[j][half], aw = x.a[i][half];
+                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    (v8i){(int)bw.x, (int)bw.y, (int)bw.z, (int)bw.w, 0, 0, 0, 0},
+                                    (v8i){(int)aw.x, (int)aw.y, (int)aw.z, (int)aw.w, 0, 0, 0, 0}, acc[i][j], 4, 4, 0,
+                                    (int)((half ? x.bs[j].y : x.bs[j].x) >> (8 * h)), 0,
+                                    (int)((half ? x.as[i].y : x.as[i].x) >> (8 * h)));
+                            }
+                } else {
 #pragma unroll
-                    for (int s = 0; s < 4; s++) {
-                        v8bf bv[NB];
+                    for (int half = 0; half < 2; half++) {
+                        float fa[MB], fb[NB];
 #pragma unroll
-                        for (int j = 0; j < NB; j++) {
-                            const uint4 w = x.b[j][half];
-                            bv[j] = cvt8_bf16_e2m1(s == 0 ? w.x : s == 1 ? w.y : s == 2 ? w.z : w.w, fb[j]);
-                        }
+                        for (int i = 0; i < MB; i++)
+                            fa[i] = scale_f32(half ? x.as[i].y : x.as[i].x);
 #pragma unroll
-                        for (int i = 0; i < MB; i++) {
-                            const uint4 w = x.a[i][2 * half + s / 2];
-                            const v8bf av = s % 2 ? cvt8_bf16(w.z, w.w, fa[i]) : cvt8_bf16(w.x, w.y, fa[i]);
+                        for (int j = 0; j < NB; j++)
+                            fb[j] = scale_f32(((half ? x.bs[j].y : x.bs[j].x) >> (8 * h)) & 0xFFu);
 #pragma unroll
-                            for (int j = 0; j < NB; j++)
-                                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av, acc[i][j], 0, 0, 0);
+                        for (int s = 0; s < 4; s++) {
+                            v8bf bv[NB];
+#pragma unroll
+                            for (int j = 0; j < NB; j++) {
+                                const uint4 w = x.b[j][half];
+                                bv[j] = cvt8_bf16_e2m1(s == 0 ? w.x : s == 1 ? w.y : s == 2 ? w.z : w.w, fb[j]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < MB; i++) {
+                                const uint4 w = x.a[i][2 * half + s / 2];
+                                const v8bf av = s % 2 ? cvt8_bf16(w.z, w.w, fa[i]) : cvt8_bf16(w.x, w.y, fa[i]);
+#pragma unroll
+                                for (int j = 0; j < NB; j++)
+                                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av, acc[i][j], 0, 0, 0);
+                            }
                         }
                     }
                 }
-            }
-        };
-        if (wave < units) {
-            NarrowUnit<A8, MB, NB> x;
-            load(wave, x);
-            int u = wave;
-            for (; u + W < units; u += W) {
-                NarrowUnit<A8, MB, NB> next;
-                load(u + W, next);
+            };
+            if (wave < units) {
+                NarrowUnit<A8, MB, NB> x;
+                load(wave, x);
+                int u = wave;
+                for (; u + W < units; u += W) {
+                    NarrowUnit<A8, MB, NB> next;
+                    load(u + W, next);
+                    product(u, x);
+                    x = next;
+                }
                 product(u, x);
-                x = next;
             }
-            product(u, x);
-        }
 #pragma unroll
-        for (int i = 0; i < MB; i++)
+            for (int i = 0; i < MB; i++)
 #pragma unroll
-            for (int j = 0; j < NB; j++)
-                part[wave][i * NB + j][lane] = acc[i][j];
-        __syncthreads();
-        // register t of lane l: column (l / 16) * 4 + t, row l % 16 of a 16 x 16 block
-        for (int o = threadIdx.x; o < MB * NB * 64; o += W * 64) {
-            const int blk = o >> 6, l = o & 63;
-            v4f sum = part[0][blk][l];
+                for (int j = 0; j < NB; j++)
+                    part[wave][i * NB + j][lane] = acc[i][j];
+            __syncthreads();
+            // register t of lane l: column (l / 16) * 4 + t, row l % 16 of a 16 x 16 block
+            for (int o = threadIdx.x; o < MB * NB * 64; o += W * 64) {
+                const int blk = o >> 6, l = o & 63;
+                v4f sum = part[0][blk][l];
 #pragma unroll
-            for (int w = 1; w < W; w++)
-                sum += part[w][blk][l];
-            const int64_t m = m0 + (blk / NB) * 16 + (l & 15), n = n0 + (blk % NB) * 16 + (l >> 4) * 4;
-            if (m < hi) {
-                const int64_t at = m * p.ldd + n;
+                for (int w = 1; w < W; w++)
+                    sum += part[w][blk][l];
+                const int64_t m = m0 + (blk / NB) * 16 + (l & 15), n = n0 + (blk % NB) * 16 + (l >> 4) * 4;
+                if (m < hi) {
+                    const int64_t at = m * p.ldd + n;
 #pragma unroll
-                for (int t = 0; t < 4; t++)
-                    if (n + t < p.N) {
-                        if constexpr (OUT_BF16)
-                            ((__bf16 *)p.d)[at + t] = (__bf16)sum[t];
-                        else
-                            ((float *)p.d)[at + t] = p.accumulate ? ((float *)p.d)[at + t] + sum[t] : sum[t];
-                    }
+                    for (int t = 0; t < 4; t++)
+                        if (n + t < p.N) {
+                            if constexpr (OUT_BF16)
+                                ((__bf16 *)p.d)[at + t] = (__bf16)sum[t];
+                            else
+                                ((float *)p.d)[at + t] = p.accumulate ? ((float *)p.d)[at + t] + sum[t] : sum[t];
+                        }
+                }
             }
+            __syncthreads();
         }
-        __syncthreads();
+        if (!p.offs)
+            return;
     }
 }
 
@@ -249,7 +254,8 @@ template <bool A8, int MB, int NB, int W> static void launch_narrow(const Mx4Arg
     const int tiles_n = (int)((p.N + 16 * NB - 1) / (16 * NB));
     const int64_t all = (p.M + 16 * MB - 1) / (16 * MB);
     const int chunks = p.offs ? 1 : (int)(all < 64 ? all : 64); // (experts' rows: a workgroup takes all)
-    const int64_t grid = (int64_t)((tiles_n + 7) / 8) * 8 * chunks * p.G;
+    const int64_t pairs = (int64_t)tiles_n * p.G;
+    const int64_t grid = p.offs ? (pairs < 512 ? pairs : 512) : (int64_t)((tiles_n + 7) / 8) * 8 * chunks;
     if (bf16)
         mx4_narrow_kernel<A8, MB, NB, W, true><<<(unsigned)grid, W * 64, 0, st>>>(p, tiles_n, chunks);
     else
@@ -337,7 +343,7 @@ static int launch_mx4(const char *name, const Mx4Args &p, int a_fmt, int d_dtype
     // 16-row blocks, per expert for a grouped product: half a padding to 16 off the
     // average, since M_cap is a bound
     const int64_t rows = p.offs ? p.M / p.G - 8 : p.M, blocks = rows > 16 ? (rows + 15) / 16 : 1;
-    FGB_REQUIRE((p.N / 16 + 8) * 64 * p.G < (1ll << 31), FGB_EINVAL, "%s: too many tiles", name);
+    FGB_REQUIRE((p.N / 16 + 8) * 64 < (1ll << 31), FGB_EINVAL, "%s: too many tiles", name);
     if (a_fmt == FGB_E4M3)
         launch_narrow_for<true>(p, blocks, bf16, st);
     else

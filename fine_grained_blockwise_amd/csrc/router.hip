@@ -340,59 +340,91 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
 }
 
 // Counts and loss from the workgroups' partial results: 32 experts a workgroup, 32
-// threads to an expert, added in order.  The workgroup that comes last (the ticket,
-// zeroed by the forward kernel) adds the workgroups' parts of the loss, in order too.
-// One workgroup for all experts moved its 1 MB (512 partial results of 257 experts) at
-// one CU's rate: 60 us.
+// threads to an expert, added in order; the first workgroup takes the live tokens too.
+// Up to 32 experts one workgroup writes the loss; beyond, the one that comes last (the
+// ticket, zeroed by the forward kernel) adds the workgroups' parts, in order too.  One
+// workgroup for all of 257 experts moved its 1 MB (512 partial results) at one CU's
+// rate: 60 us against 7.
 constexpr int RED_COLS = 32, RED_SLICES = 32;
 __global__ __launch_bounds__(RED_COLS * RED_SLICES) void router_reduce_kernel(RouterArgs a, int blocks)
 {
-    __shared__ double fsum[RED_SLICES][RED_COLS];
-    __shared__ int csum[RED_SLICES][RED_COLS];
+    __shared__ double fsum[RED_SLICES / 2][RED_COLS];
+    __shared__ int csum[RED_SLICES / 2][RED_COLS], lsum[RED_SLICES / 2];
     const int col = threadIdx.x % RED_COLS, slice = threadIdx.x / RED_COLS;
     const int e = blockIdx.x * RED_COLS + col;
-    int c = 0;
+    const bool on = e < a.E;
+    const int ec = on ? e : a.E - 1;
+    int c = 0, live = 0;
     double f = 0.0;
-    if (e <= a.E) {
-#pragma unroll 4
-        for (int b = slice; b < blocks; b += RED_SLICES)
-            c += a.pcnt[(int64_t)b * (a.E + 1) + e];
-    }
-    if (a.loss && e < a.E) {
-#pragma unroll 4
-        for (int b = slice; b < blocks; b += RED_SLICES)
-            f += a.psum[(int64_t)b * a.E + e];
-    }
-    csum[slice][col] = c;
-    fsum[slice][col] = f;
-    __syncthreads();
-    if (slice == 0) {
-        c = 0;
-        f = 0.0;
-        for (int s = 0; s < RED_SLICES; s++) {
-            c += csum[s][col];
-            f += fsum[s][col];
+    // eight partial results in flight at a time: loads without branches, the last one
+    // again past the end
+    for (int b0 = slice; b0 < blocks; b0 += 8 * RED_SLICES) {
+        int ci[8], li[8] = {};
+        float fi[8] = {};
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            ci[i] = a.pcnt[(int64_t)min(b0 + i * RED_SLICES, blocks - 1) * (a.E + 1) + ec];
+        if (a.loss) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                fi[i] = a.psum[(int64_t)min(b0 + i * RED_SLICES, blocks - 1) * a.E + ec];
         }
-        if (e <= a.E)
-            a.counts[e] = c;
-        fsum[0][col] = e < a.E ? (double)c * f : 0.0;
+        if (blockIdx.x == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                li[i] = a.pcnt[(int64_t)min(b0 + i * RED_SLICES, blocks - 1) * (a.E + 1) + a.E];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const bool in = b0 + i * RED_SLICES < blocks;
+            c += in ? ci[i] : 0;
+            live += in ? li[i] : 0;
+            f += in ? fi[i] : 0.0f;
+        }
     }
+    // two slices to a wave, then the waves in order
+    c += __shfl_xor(c, 32);
+    f += __shfl_xor(f, 32);
+    live += __shfl_xor(live, 32);
+    if ((slice & 1) == 0) {
+        csum[slice / 2][col] = c;
+        fsum[slice / 2][col] = f;
+        if (col == 0)
+            lsum[slice / 2] = live;
+    }
+    __syncthreads();
+    if (threadIdx.x >= RED_COLS)
+        return;
+    c = live = 0;
+    f = 0.0;
+#pragma unroll
+    for (int s = 0; s < RED_SLICES / 2; s++) {
+        c += csum[s][col];
+        live += lsum[s];
+        f += fsum[s][col];
+    }
+    if (on)
+        a.counts[e] = c;
+    double part = on ? (double)c * f : 0.0;
+#pragma unroll
+    for (int d = RED_COLS / 2; d >= 1; d >>= 1)
+        part += __shfl_xor(part, d);
+    if (threadIdx.x != 0)
+        return;
+    if (blockIdx.x == 0)
+        __hip_atomic_store(&a.counts[a.E], live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (!a.loss)
         return;
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    if (gridDim.x == 1) {
+        write_loss(a, part, live);
+        return;
+    }
+    __hip_atomic_store(&a.lpart[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1) {
         double sum = 0.0;
-        for (int i = 0; i < RED_COLS; i++)
-            sum += fsum[0][i];
-        a.lpart[blockIdx.x] = sum;
-        __threadfence(); // this workgroup's count of live tokens and part, before the ticket
-        if (atomicAdd(a.ticket, 1) == (int)gridDim.x - 1) {
-            __threadfence();
-            double parts = 0.0;
-            for (int i = 0; i < (int)gridDim.x; i++)
-                parts += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            write_loss(a, parts, __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        }
+        for (int i = 0; i < (int)gridDim.x; i++)
+            sum += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        write_loss(a, sum, __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     }
 }
 
@@ -520,7 +552,7 @@ static int64_t router_blocks(int64_t T, int E)
     return n < 1 ? 1 : n < 1024 ? n : 1024;
 }
 
-static int reduce_blocks(int E) { return (E + RED_COLS) / RED_COLS; }
+static int reduce_blocks(int E) { return (E + RED_COLS - 1) / RED_COLS; }
 
 static int check_router(const char *name, const void *z, int dtype, int64_t T, int E, int64_t ldz, int k, int score)
 {

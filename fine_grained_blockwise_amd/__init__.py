@@ -904,9 +904,16 @@ def mx2_dequant(q, s2, s1, g1=10240):
 
 
 # ---------------------------------------------------------------------------
-def _mxfp4_shapes(rows, cols):
-    """Shapes of the codes and scales of an MXFP4 tensor of `rows` x `cols` values."""
-    return (rows, cols // 2), ((cols + 255) // 256, rows, 8)
+def _all_u8(*pairs):
+    """Whether each (tensor, shape) is a contiguous uint8 tensor of that shape: the usual case in one pass; the checks
+    that name what is wrong run only otherwise."""
+    for t, shape in pairs:
+        if t is None or t.dtype is not _U8 or t.shape != shape or not t.is_contiguous():
+            return False
+    return True
+
+
+_U8 = torch.uint8
 
 
 def _mxfp4_input(x, name):
@@ -938,8 +945,8 @@ def mxfp4_quant(x, rule=SCALE_CEIL):
     see include/fgb.h for the layouts."""
     x, lead, rows, cols = _mxfp4_input(x, "mxfp4_quant")
     q, s = _mxfp4_out(lead, rows, cols, x.device)
-    _call("mxfp4_quant", _ptr(x), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule, _ptr(q),
-          _ptr(s), _stream(x))
+    _call("mxfp4_quant", x.data_ptr(), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule,
+          q.data_ptr(), s.data_ptr(), _stream(x))
     return q, s
 
 
@@ -950,51 +957,59 @@ def mxfp4_quant_t(x, rule=SCALE_CEIL):
     x, lead, rows, cols = _mxfp4_input(x, "mxfp4_quant_t")
     q, s = _mxfp4_out(lead, rows, cols, x.device)
     qt, st = _mxfp4_out(lead, cols, (rows + 31) // 32 * 32, x.device)
-    _call("mxfp4_quant_t", _ptr(x), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule, _ptr(q),
-          _ptr(s), _ptr(qt), _ptr(st), _stream(x))
+    _call("mxfp4_quant_t", x.data_ptr(), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule,
+          q.data_ptr(), s.data_ptr(), qt.data_ptr(), st.data_ptr(), _stream(x))
     return q, s, qt, st
 
 
 def mxfp4_dequant(q, s, out_dtype=torch.float32):
     """decode(q) * 2^(s-127) -> [rows, cols] (fp32 or bf16)."""
-    _check_2d_codes(q, "mxfp4_dequant: q")
-    rows, cols = q.shape[0], 2 * q.shape[1]
-    _need(s, "mxfp4_dequant: s", shape=_mxfp4_shapes(rows, cols)[1], dtype=torch.uint8, contiguous=True)
-    _need(q, "mxfp4_dequant: q", contiguous=True)
-    _out_dtype(out_dtype, "mxfp4_dequant")
+    if q.dim() != 2:
+        raise ValueError("mxfp4_dequant: q must be 2-D")
+    rows, half = q.shape
+    cols = 2 * half
+    if not _all_u8((q, (rows, half)), (s, ((cols + 255) // 256, rows, 8))):
+        _need(q, "mxfp4_dequant: q", dtype=_U8, contiguous=True)
+        _need(s, "mxfp4_dequant: s", shape=((cols + 255) // 256, rows, 8), dtype=_U8, contiguous=True)
     _check_dev(q, s)
+    _out_dtype(out_dtype, "mxfp4_dequant")
     out = torch.empty(rows, cols, dtype=out_dtype, device=q.device)
-    _call("mxfp4_dequant", _ptr(q), _ptr(s), rows, cols, _ptr(out), _dtype_code(out), _stream(q))
+    _call("mxfp4_dequant", q.data_ptr(), s.data_ptr(), rows, cols, out.data_ptr(), _dtype_code(out), _stream(q))
     return out
 
 
-def _mxfp4_a(a, sa, a_fmt, name):
-    """K of the A operand, its scales checked against it."""
-    _check_2d_codes(a, f"{name}: a")
+def _mxfp4_a(a, a_fmt, name):
+    """M and K of the A operand, and the shape of its scales."""
     if a_fmt not in (E2M1, E4M3):
         raise ValueError(f"{name}: a_fmt must be E2M1 or E4M3")
-    M, K = a.shape[0], a.shape[1] * (2 if a_fmt == E2M1 else 1)
-    shape = _mxfp4_shapes(M, K)[1] if a_fmt == E2M1 else (M, K // 128)
-    _need(sa, f"{name}: sa", shape=shape, dtype=torch.uint8, contiguous=True)
-    return M, K
+    if a.dim() != 2:
+        raise ValueError(f"{name}: a must be 2-D")
+    M, K = a.shape
+    if a_fmt == E4M3:
+        return M, K, (M, K // 128)
+    return M, 2 * K, ((2 * K + 255) // 256, M, 8)
 
 
 def mxfp4_gemm(a, sa, b, sb, a_fmt=E2M1, out_dtype=torch.bfloat16, d=None, accumulate=False):
     """D = A * B^T with MXFP4 weights b [N, K/2]: A in MXFP4 (a [M, K/2]) or, with a_fmt E4M3, in E4M3 codes
     [M, K] with 1x128 scales -> D [M, N]."""
     name = "mxfp4_gemm"
-    M, K = _mxfp4_a(a, sa, a_fmt, name)
-    _check_2d_codes(b, f"{name}: b")
+    M, K, sa_shape = _mxfp4_a(a, a_fmt, name)
+    if b.dim() != 2 or 2 * b.shape[1] != K:
+        raise ValueError(f"{name}: b must be [N, K/2] with the same K as a")
     N = b.shape[0]
-    if 2 * b.shape[1] != K:
-        raise ValueError(f"{name}: a and b must have the same K")
-    _need(sb, f"{name}: sb", shape=_mxfp4_shapes(N, K)[1], dtype=torch.uint8, contiguous=True)
+    sb_shape = ((K + 255) // 256, N, 8)
+    if not _all_u8((a, a.shape), (sa, sa_shape), (b, b.shape), (sb, sb_shape)):
+        _need(a, f"{name}: a", dtype=_U8)
+        _need(b, f"{name}: b", dtype=_U8)
+        _need(sa, f"{name}: sa", shape=sa_shape, dtype=_U8, contiguous=True)
+        _need(sb, f"{name}: sb", shape=sb_shape, dtype=_U8, contiguous=True)
     d = _gemm_out(d, M, N, out_dtype, name)
     _check_dev(a, sa, b, sb, d)
     if d is None:
         d = torch.empty(M, N, dtype=out_dtype, device=a.device)
-    _call(name, _ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), M, N, K, _row_ld(a), _row_ld(b), _ptr(d), _dtype_code(d),
-          _row_ld(d), int(bool(accumulate)), _stream(a))
+    _call(name, a.data_ptr(), sa.data_ptr(), a_fmt, b.data_ptr(), sb.data_ptr(), M, N, K, _row_ld(a), _row_ld(b),
+          d.data_ptr(), _dtype_code(d), _row_ld(d), 1 if accumulate else 0, _stream(a))
     return d
 
 
@@ -1002,20 +1017,21 @@ def mxfp4_grouped_gemm(a, sa, b, sb, group_offsets, a_fmt=E4M3, out_dtype=torch.
     """mxfp4_gemm per expert: rows [off[g], off[g+1]) of a [M_cap, ...] with the weights b [G, N, K/2],
     sb [G, ceil(K/256), N, 8]; offsets int32 [G+1] (device) -> d [M_cap, N]."""
     name = "mxfp4_grouped_gemm"
-    M_cap, K = _mxfp4_a(a, sa, a_fmt, name)
-    if b.dim() != 3:
-        raise ValueError(f"{name}: b must be [G, N, K/2]")
+    M_cap, K, sa_shape = _mxfp4_a(a, a_fmt, name)
+    if b.dim() != 3 or 2 * b.shape[2] != K:
+        raise ValueError(f"{name}: b must be [G, N, K/2] with the same K as a")
     G, N = b.shape[0], b.shape[1]
-    _need(a, f"{name}: a", contiguous=True)
-    _need(b, f"{name}: b", shape=(G, N, K // 2), dtype=torch.uint8, contiguous=True)
-    _need(sb, f"{name}: sb", shape=(G,) + _mxfp4_shapes(N, K)[1], dtype=torch.uint8, contiguous=True)
+    sb_shape = (G, (K + 255) // 256, N, 8)
+    if not _all_u8((a, a.shape), (sa, sa_shape), (b, b.shape), (sb, sb_shape)):
+        for t, nm, shape in ((a, "a", None), (sa, "sa", sa_shape), (b, "b", None), (sb, "sb", sb_shape)):
+            _need(t, f"{name}: {nm}", shape=shape, dtype=_U8, contiguous=True)
     _need(group_offsets, f"{name}: group_offsets", shape=(G + 1,), dtype=torch.int32, contiguous=True)
     d = _gemm_out(d, M_cap, N, out_dtype, name, contiguous=True)
     _check_dev(a, sa, b, sb, group_offsets, d)
     if d is None:
         d = torch.empty(M_cap, N, dtype=out_dtype, device=a.device)
-    _call(name, _ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), _ptr(group_offsets), G, M_cap, N, K, _ptr(d),
-          _dtype_code(d), _stream(a))
+    _call(name, a.data_ptr(), sa.data_ptr(), a_fmt, b.data_ptr(), sb.data_ptr(), group_offsets.data_ptr(), G, M_cap, N,
+          K, d.data_ptr(), _dtype_code(d), _stream(a))
     return d
 
 

@@ -144,18 +144,24 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_wave_barrier();
 }
 
-// Order-preserving map of a logit to an unsigned key and back; 0 for -inf and NaN,
-// which are never chosen.  -0 and +0 are equal logits and get one key.
-__device__ __forceinline__ uint32_t logit_key(float z)
+// Order-preserving map of expert e's logit to an unsigned key and back; 0 for -inf and
+// NaN, which are never chosen.  -0 and +0 are equal logits and get one key.  A bf16
+// logit's key needs 16 bits; the 16 below them hold the id, the lowest as the largest,
+// so that one maximum chooses and names the expert.
+template <bool BF16> __device__ __forceinline__ uint32_t logit_key(float z, int e)
 {
     const uint32_t u = __float_as_uint(z == 0.0f ? 0.0f : z);
-    const uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
+    uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
+    if constexpr (BF16)
+        key = (key | 0xFFFFu) - (uint32_t)e;
     return z > NEG_INF ? key : 0u;
 }
-__device__ __forceinline__ float key_logit(uint32_t key)
+template <bool BF16> __device__ __forceinline__ float key_logit(uint32_t key)
 {
-    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+    const uint32_t u = (key >> 31) ? key & 0x7FFFFFFFu : ~key;
+    return __uint_as_float(BF16 ? u & 0xFFFF0000u : u);
 }
+__device__ __forceinline__ int key_expert_bf16(uint32_t key) { return (int)(~key & 0xFFFFu); }
 
 // What a token's scores are formed with: for softmax m = max z and inv = 1 / sum
 // exp(z - m), for sigmoid m = min(0, max z) and inv = 1 / sum t.
@@ -163,20 +169,25 @@ struct Norm {
     float m, inv;
 };
 
+// Sigmoid s and its complement, from one exponential and one reciprocal (of a number
+// in [1, 2], to one unit in the last place).
+struct Sig {
+    float s, one_minus, r; // r = 1 / (1 + exp(-|z|))
+};
+__device__ __forceinline__ Sig sigmoid(float z)
+{
+    const float a = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + a);
+    return z > 0.0f ? Sig{r, a * r, r} : Sig{a * r, r, r};
+}
 // exp(z - m) (softmax: s before its division), or the sigmoid's numerator
-// t = exp(z - m) / (1 + exp(z)), in the form that neither over- nor underflows.
+// t = exp(z - m) / (1 + exp(z)), in the form that neither over- nor underflows:
+// s itself where a logit of the token is above 0.
 template <int SCORE> __device__ __forceinline__ float numerator(float z, float m)
 {
     if constexpr (SCORE == FGB_ROUTER_SOFTMAX)
         return expf(z - m);
-    const float d = 1.0f + expf(-fabsf(z));
-    return z > 0.0f ? 1.0f / d : expf(z - m) / d;
-}
-// sigmoid(z) itself (a weight without renorm).
-__device__ __forceinline__ float sigmoid(float z)
-{
-    const float a = expf(-fabsf(z));
-    return (z > 0.0f ? 1.0f : a) / (1.0f + a);
+    const Sig g = sigmoid(z);
+    return m < 0.0f ? expf(z - m) * g.r : g.s;
 }
 
 // The loss from sum_e counts_e sum_t p_te.
@@ -186,20 +197,34 @@ __device__ __forceinline__ void write_loss(const RouterArgs &a, double sum, int 
     *a.loss = (float)((double)a.coef * a.E / (a.k * n * n) * sum);
 }
 
-// p of the lane's experts (num: the numerators), top the group's largest key.
+// p of the lane's experts (num: the numerators; sg: the sigmoids, for that score), m
+// the largest logit of the group.
 template <int SCORE, int L, int R>
-__device__ __forceinline__ Norm probabilities(const float (&z)[R], uint32_t top, float (&num)[R], float (&p)[R])
+__device__ __forceinline__ Norm probabilities(const float (&z)[R], float m, float (&num)[R], float (&p)[R], Sig (&sg)[R])
 {
     Norm n;
-    n.m = key_logit(top);
-    if constexpr (SCORE == FGB_ROUTER_SIGMOID)
-        n.m = fminf(n.m, 0.0f);
+    n.m = m;
     float sum = 0.0f;
+    if constexpr (SCORE == FGB_ROUTER_SIGMOID) {
+        n.m = fminf(m, 0.0f);
 #pragma unroll
-    for (int j = 0; j < R; j++) {
-        num[j] = numerator<SCORE>(z[j], n.m);
-        sum += num[j];
+        for (int j = 0; j < R; j++) {
+            sg[j] = sigmoid(z[j]);
+            num[j] = sg[j].s;
+        }
+        if (__any(n.m < 0.0f)) { // a token of the wave without a logit above 0
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                num[j] = n.m < 0.0f ? expf(z[j] - n.m) * sg[j].r : num[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < R; j++)
+            num[j] = expf(z[j] - n.m);
     }
+#pragma unroll
+    for (int j = 0; j < R; j++)
+        sum += num[j];
     n.inv = 1.0f / group_sum<L>(sum);
 #pragma unroll
     for (int j = 0; j < R; j++)
@@ -214,6 +239,7 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
     constexpr int GROUPS = 256 / L;
     const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = l * R;
     int *cnt = reinterpret_cast<int *>(red + (a.loss ? GROUPS * a.E : 0));
+    __shared__ int ids[BF16 ? 1 : 256]; // [groups][L]
     for (int e = threadIdx.x; e <= a.E; e += 256)
         cnt[e] = 0;
     __syncthreads();
@@ -236,47 +262,58 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
         }
 #pragma unroll
         for (int j = 0; j < R; j++) {
-            key[j] = on ? logit_key(z[j]) : 0u;
+            key[j] = on ? logit_key<BF16>(z[j], e0 + j) : 0u;
             best = max(best, key[j]);
         }
         uint32_t top = group_max<L>(best);
         const uint32_t first = top; // 0: the token is not live
-        // topk rounds; lane r keeps the r-th choice's logit and id
+        // topk rounds; lane r keeps the r-th choice's key (and, through LDS, its id)
         uint32_t mine = 0;
-        int mine_e = -1;
         for (int r = 0; r < a.k; r++) {
-            // the lowest lane with the largest key, its lowest position
-            const uint64_t hits = __ballot(best == top && top != 0);
-            const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
-                                    : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
-                                                    (L == 32 ? 0x80000000u : 1u << (L & 31)));
-            const bool won = l == win && best == top && top != 0;
-            int at = 0;
-            uint32_t rest = 0;
-            bool look = won;
+            mine = l == r ? top : mine;
+            best = 0;
+            if constexpr (BF16) { // one expert has this key (no expert: all have 0)
 #pragma unroll
-            for (int j = 0; j < R; j++) {
-                const bool hit = look && key[j] == top;
-                at = hit ? j : at;
-                key[j] = hit ? 0u : key[j];
-                look = look && !hit;
-                rest = max(rest, key[j]);
+                for (int j = 0; j < R; j++) {
+                    key[j] = key[j] == top ? 0u : key[j];
+                    best = max(best, key[j]);
+                }
+            } else { // the lowest lane with the largest key, its lowest position
+                int at = R;
+#pragma unroll
+                for (int j = R - 1; j >= 0; j--)
+                    at = key[j] == top ? j : at;
+                const uint64_t hits = __ballot(at < R);
+                const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
+                                        : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
+                                                        (L == 32 ? 0x80000000u : 1u << (L & 31)));
+                at = l == win ? at : R;
+                if (at < R)
+                    ids[group * L + r] = e0 + at;
+#pragma unroll
+                for (int j = 0; j < R; j++) {
+                    key[j] = j == at ? 0u : key[j];
+                    best = max(best, key[j]);
+                }
             }
-            if (won)
-                atomicAdd(&cnt[e0 + at], 1); // integers: any order gives the same counts
-            // every lane of the group learns the id: one lane holds it, the others 0
-            const int e = (int)group_max<L>(won ? (uint32_t)(e0 + at + 1) : 0u) - 1;
-            if (l == r) {
-                mine = top;
-                mine_e = e;
-            }
-            best = rest;
             top = group_max<L>(best);
         }
+        int mine_e = -1;
+        if constexpr (BF16) {
+            mine_e = mine ? key_expert_bf16(mine) : -1;
+        } else {
+            wave_sync();
+            if (mine)
+                mine_e = ids[threadIdx.x];
+            wave_sync();
+        }
+        if (mine)
+            atomicAdd(&cnt[mine_e], 1); // integers: any order gives the same counts
         float num[R], p[R];
-        const Norm n = probabilities<SCORE, L, R>(z, first, num, p);
+        Sig sg[R];
+        const Norm n = probabilities<SCORE, L, R>(z, key_logit<BF16>(first), num, p, sg);
         // lane r: the weight of slot r
-        const float zr = key_logit(mine);
+        const float zr = key_logit<BF16>(mine);
         const float nr = mine ? numerator<SCORE>(zr, n.m) : 0.0f;
         float w = nr * n.inv;
         if (a.renorm) {
@@ -284,7 +321,7 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
             // (a NaN logit is not chosen, but must not go unseen either)
             w = n.inv == n.inv ? w : n.inv;
         } else if (SCORE == FGB_ROUTER_SIGMOID) {
-            w = sigmoid(zr);
+            w = sigmoid(zr).s;
         }
         if (t < a.T && l < a.k) {
             a.idx[t * a.k + l] = mine_e;
@@ -472,16 +509,17 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             const uint32_t u = mine[e0 + j];
             on[j] = u != NOT_CHOSEN;
             d[j] = on[j] ? __uint_as_float(u) : 0.0f;
-            best = max(best, logit_key(z[j]));
+            best = max(best, logit_key<BF16>(z[j], e0 + j));
         }
         const bool live = group_max<L>(slot >= 0 ? 1u : 0u) != 0;
         float num[R], p[R], dz[R];
-        probabilities<SCORE, L, R>(z, group_max<L>(best), num, p);
+        Sig sg[R];
+        probabilities<SCORE, L, R>(z, key_logit<BF16>(group_max<L>(best)), num, p, sg);
         float gp = 0.0f, chosen = 0.0f, dv = 0.0f, v[R];
 #pragma unroll
         for (int j = 0; j < R; j++) {
             gp += g[j] * p[j];
-            v[j] = !on[j] ? 0.0f : a.renorm ? num[j] : SCORE == FGB_ROUTER_SIGMOID ? sigmoid(z[j]) : p[j];
+            v[j] = !on[j] ? 0.0f : a.renorm ? num[j] : SCORE == FGB_ROUTER_SIGMOID ? sg[j].s : p[j];
             chosen += v[j];
             dv += d[j] * v[j];
         }
@@ -500,9 +538,8 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
                 if (!a.renorm)
                     q -= p[j] * dv;
             } else {
-                const float one_minus = sigmoid(-z[j]); // 1 - s
-                w *= one_minus;
-                q *= one_minus;
+                w *= sg[j].one_minus;
+                q *= sg[j].one_minus;
             }
             dz[j] = !live ? 0.0f : on[j] ? q + w : q;
         }

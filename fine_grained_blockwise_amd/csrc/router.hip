@@ -20,25 +20,30 @@
 // A renormed sigmoid weight is formed from exp(z - m) / (1 + exp(z)), m =
 // min(0, max z), so that logits far below zero do not divide zero by zero.
 //
-// L lanes (8, 16, 32 or 64) take a token, lane l of them experts l R .. l R + R - 1:
-// the smallest L with L R >= E at R = 4, at least topk (lane j ends with slot j), so
-// a wave of a 32-expert router handles eight tokens at once.  A choice is a maximum
-// over the L lanes; its logit is read back from the winning key, so nothing is
-// broadcast.  All sums are fp32 in a fixed order (the last, over workgroups, in
-// fp64): results do not depend on timing.  Launches and instruction issue bound it:
-// 16384 x 32 logits are 2 MB.
+// L lanes (8, 16, 32 or 64, at least topk: lane j ends with slot j) take a token, so a
+// wave of a 32-expert router handles eight tokens at once.  A lane holds Q <= 4 quads of
+// experts, quad q of lane l being 4 (q L + l) .. + 3: a load, a store and an access to LDS
+// each touch one run of memory (4999 x 257 bf16: forward with loss 19.4 us with a lane's
+// experts in one run of 16, 16.3 us so; 32768 x 1024 backward 75 and 49 us).  A choice is
+// a maximum over the L lanes; its logit is read back from the winning key.  All sums are
+// fp32 in a fixed order (the last, over workgroups, in fp64): results do not depend on
+// timing.  Launches and instruction issue bound it: 16384 x 32 logits are 2 MB.
 #include "fgb_internal.h"
 
 namespace fgb {
 
 constexpr float NEG_INF = -__builtin_inff();
+constexpr int NOWHERE = 0x7FFFFFF;
+
+// Expert of a lane's j-th logit, less the lane's first (four times the lane).
+template <int L> constexpr __device__ int at_quad(int j) { return j / 4 * 4 * L + j % 4; }
 
 struct RouterArgs {
     const void *z;
     int64_t T, ldz;
     int E, k;
     const uint8_t *mask;
-    int renorm, vec, vecd; // vec, vecd: rows of z, dz are whole aligned vectors
+    int renorm;
     float scale, coef;
     int32_t *idx;
     float *w;
@@ -56,49 +61,53 @@ struct RouterArgs {
     int64_t lddz;
 };
 
-// The lane's R logits of a token; vec: rows are whole aligned vectors of R.
-template <bool BF16, int R>
-__device__ __forceinline__ void load_logits(const RouterArgs &a, int64_t t, int e0, float (&z)[R])
+// The lane's logits of token t, -inf past the last expert.  Only the last quad can
+// reach past it (4 L (Q - 1) < E): it is read from where four experts are left and
+// moved up.  (Rows need no alignment beyond the type's: the card's loads do not.)
+template <bool BF16, int L, int Q>
+__device__ __forceinline__ void load_logits(const RouterArgs &a, int64_t t, int e0, float (&z)[4 * Q])
 {
-    if (a.vec) {
-        if (e0 >= a.E) {
+    const int64_t row = t * a.ldz;
+    if (a.E < 4) { // uniform
 #pragma unroll
-            for (int j = 0; j < R; j++)
-                z[j] = NEG_INF;
-        } else if constexpr (BF16) {
-            uint32_t w[R / 2];
-            const uint16_t *p = (const uint16_t *)a.z + t * a.ldz + e0;
-#pragma unroll
-            for (int j = 0; j < R / 4; j++) {
-                const uint2 u = reinterpret_cast<const uint2 *>(p)[j];
-                w[2 * j] = u.x;
-                w[2 * j + 1] = u.y;
-            }
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                z[j] = j % 2 ? bf16hi(w[j / 2]) : bf16lo(w[j / 2]);
-        } else {
-            const float *p = (const float *)a.z + t * a.ldz + e0;
-#pragma unroll
-            for (int j = 0; j < R / 4; j++) {
-                const float4 u = reinterpret_cast<const float4 *>(p)[j];
-                z[4 * j] = u.x;
-                z[4 * j + 1] = u.y;
-                z[4 * j + 2] = u.z;
-                z[4 * j + 3] = u.w;
-            }
+        for (int i = 0; i < 4; i++) {
+            z[i] = NEG_INF;
+            if (e0 + i < a.E)
+                z[i] = BF16 ? __uint_as_float((uint32_t)((const uint16_t *)a.z)[row + e0 + i] << 16)
+                            : ((const float *)a.z)[row + e0 + i];
         }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < R; j++) {
-        const int e = e0 + j;
-        if (e >= a.E)
-            z[j] = NEG_INF;
-        else if constexpr (BF16)
-            z[j] = __uint_as_float((uint32_t)((const uint16_t *)a.z)[t * a.ldz + e] << 16);
-        else
-            z[j] = ((const float *)a.z)[t * a.ldz + e];
+    for (int q = 0; q < Q; q++) {
+        const int e = q < Q - 1 ? e0 + 4 * L * q : min(e0 + 4 * L * q, a.E - 4);
+        if constexpr (BF16) {
+            uint2 u;
+            __builtin_memcpy(&u, (const uint16_t *)a.z + row + e, 8);
+            z[4 * q] = bf16lo(u.x);
+            z[4 * q + 1] = bf16hi(u.x);
+            z[4 * q + 2] = bf16lo(u.y);
+            z[4 * q + 3] = bf16hi(u.y);
+        } else {
+            __builtin_memcpy(&z[4 * q], (const float *)a.z + row + e, 16);
+        }
+    }
+    constexpr int j = 4 * (Q - 1);
+    const int past = e0 + 4 * L * (Q - 1) - (a.E - 4); // experts of the lane's last quad past the last one
+    if (a.E & 3) {                                     // uniform
+#pragma unroll
+        for (int n = 0; n < 3; n++) { // move up by one, past times
+            const bool move = past > n;
+            z[j] = move ? z[j + 1] : z[j];
+            z[j + 1] = move ? z[j + 2] : z[j + 1];
+            z[j + 2] = move ? z[j + 3] : z[j + 2];
+            z[j + 3] = move ? NEG_INF : z[j + 3];
+        }
+    }
+    if (past >= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            z[j + i] = NEG_INF;
     }
 }
 
@@ -232,12 +241,12 @@ __device__ __forceinline__ Norm probabilities(const float (&z)[R], float m, floa
     return n;
 }
 
-template <bool BF16, int SCORE, int L, int R>
+template <bool BF16, int SCORE, int L, int Q>
 __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
 {
     extern __shared__ float red[]; // [groups][E] floats (the loss's sums), then E + 1 ints
-    constexpr int GROUPS = 256 / L;
-    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = l * R;
+    constexpr int GROUPS = 256 / L, R = 4 * Q;
+    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = 4 * l;
     int *cnt = reinterpret_cast<int *>(red + (a.loss ? GROUPS * a.E : 0));
     __shared__ int ids[BF16 ? 1 : 256]; // [groups][L]
     for (int e = threadIdx.x; e <= a.E; e += 256)
@@ -253,16 +262,10 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
         const bool on = t < a.T && (!a.mask || a.mask[t] != 0);
         float z[R];
         uint32_t key[R], best = 0;
-        if (t < a.T) {
-            load_logits<BF16, R>(a, t, e0, z);
-        } else {
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                z[j] = NEG_INF;
-        }
+        load_logits<BF16, L, Q>(a, min(t, a.T - 1), e0, z);
 #pragma unroll
         for (int j = 0; j < R; j++) {
-            key[j] = on ? logit_key<BF16>(z[j], e0 + j) : 0u;
+            key[j] = on ? logit_key<BF16>(z[j], e0 + at_quad<L>(j)) : 0u;
             best = max(best, key[j]);
         }
         uint32_t top = group_max<L>(best);
@@ -278,21 +281,27 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
                     key[j] = key[j] == top ? 0u : key[j];
                     best = max(best, key[j]);
                 }
-            } else { // the lowest lane with the largest key, its lowest position
-                int at = R;
+            } else {
+                int at = NOWHERE; // the lane's lowest id with the largest key, less e0
 #pragma unroll
                 for (int j = R - 1; j >= 0; j--)
-                    at = key[j] == top ? j : at;
-                const uint64_t hits = __ballot(at < R);
-                const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
-                                        : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
-                                                        (L == 32 ? 0x80000000u : 1u << (L & 31)));
-                at = l == win ? at : R;
-                if (at < R)
+                    at = key[j] == top ? at_quad<L>(j) : at;
+                const uint64_t some = __ballot(top != 0), hits = some & __ballot(at != NOWHERE);
+                if constexpr (Q == 1) { // ids grow with the lane: the lowest lane's
+                    const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
+                                            : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
+                                                            (L == 32 ? 0x80000000u : 1u << (L & 31)));
+                    at = l == win ? at : NOWHERE;
+                } else if (__builtin_popcountll(hits) * L > __builtin_popcountll(some)) {
+                    // equal logits in several lanes of a token
+                    const int lowest = ~(int)group_max<L>(at == NOWHERE ? 0u : ~(uint32_t)(e0 + at));
+                    at = e0 + at == lowest ? at : NOWHERE;
+                }
+                if (at != NOWHERE)
                     ids[group * L + r] = e0 + at;
 #pragma unroll
                 for (int j = 0; j < R; j++) {
-                    key[j] = j == at ? 0u : key[j];
+                    key[j] = at == at_quad<L>(j) ? 0u : key[j];
                     best = max(best, key[j]);
                 }
             }
@@ -339,8 +348,8 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
     if (a.loss) {
 #pragma unroll
         for (int j = 0; j < R; j++)
-            if (e0 + j < a.E)
-                red[group * a.E + e0 + j] = psum[j];
+            if (e0 + at_quad<L>(j) < a.E)
+                red[group * a.E + e0 + at_quad<L>(j)] = psum[j];
     }
     __syncthreads();
     // the workgroup's counts and sums, groups in order; a lone workgroup finishes
@@ -465,56 +474,59 @@ __global__ __launch_bounds__(RED_COLS * RED_SLICES) void router_reduce_kernel(Ro
     }
 }
 
-template <bool BF16, int SCORE, int L, int R>
+template <bool BF16, int SCORE, int L, int Q>
 __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
 {
-    extern __shared__ float lds[]; // [groups][L R]: D of the chosen experts
-    constexpr int GROUPS = 256 / L;
+    extern __shared__ uint4 lds[]; // [groups][4 L Q]: D of the chosen experts
+    constexpr int GROUPS = 256 / L, R = 4 * Q;
     constexpr uint32_t NOT_CHOSEN = 0xFFFFFFFFu; // a NaN that D is never left as
-    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = l * R;
-    uint32_t *mine = reinterpret_cast<uint32_t *>(lds) + group * (L * R);
+    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = 4 * l;
+    uint4 *quads = lds + group * (L * Q);
+    uint32_t *mine = reinterpret_cast<uint32_t *>(quads);
     const int n = a.counts[a.E];
     const float dl = a.dloss ? *a.dloss : 0.0f;
     const float f = n > 0 ? (float)((double)dl * a.coef * a.E / ((double)a.k * n * n)) : 0.0f;
     float g[R];
 #pragma unroll
     for (int j = 0; j < R; j++)
-        g[j] = e0 + j < a.E ? f * (float)a.counts[e0 + j] : 0.0f;
+        g[j] = f * (float)a.counts[min(e0 + at_quad<L>(j), a.E)]; // (past the last expert p is 0)
     for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
         const int64_t t = t0 + group;
         const int slot = t < a.T && l < a.k ? a.idx[t * a.k + l] : -1;
         float z[R];
-        if (t < a.T) {
-            load_logits<BF16, R>(a, t, e0, z);
-        } else {
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                z[j] = NEG_INF;
-        }
+        load_logits<BF16, L, Q>(a, min(t, a.T - 1), e0, z);
         float D = slot >= 0 && a.dw ? a.scale * a.dw[t * a.k + l] : 0.0f;
         D = D == D ? D : __builtin_nanf("");
         // to the lanes of the chosen experts, through LDS (one wave's accesses are in order)
 #pragma unroll
-        for (int j = 0; j < R; j++)
-            mine[e0 + j] = NOT_CHOSEN;
+        for (int q = 0; q < Q; q++)
+            quads[q * L + l] = make_uint4(NOT_CHOSEN, NOT_CHOSEN, NOT_CHOSEN, NOT_CHOSEN);
         wave_sync();
         if (slot >= 0 && slot < a.E)
             mine[slot] = __float_as_uint(D);
         wave_sync();
+        uint32_t u[R];
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            const uint4 w = quads[q * L + l];
+            u[4 * q] = w.x;
+            u[4 * q + 1] = w.y;
+            u[4 * q + 2] = w.z;
+            u[4 * q + 3] = w.w;
+        }
         float d[R];
         bool on[R];
         uint32_t best = 0;
 #pragma unroll
         for (int j = 0; j < R; j++) {
-            const uint32_t u = mine[e0 + j];
-            on[j] = u != NOT_CHOSEN;
-            d[j] = on[j] ? __uint_as_float(u) : 0.0f;
-            best = max(best, logit_key<BF16>(z[j], e0 + j));
+            on[j] = u[j] != NOT_CHOSEN;
+            d[j] = on[j] ? __uint_as_float(u[j]) : 0.0f;
+            best = max(best, logit_key<false>(z[j], 0));
         }
         const bool live = group_max<L>(slot >= 0 ? 1u : 0u) != 0;
         float num[R], p[R], dz[R];
         Sig sg[R];
-        probabilities<SCORE, L, R>(z, key_logit<BF16>(group_max<L>(best)), num, p, sg);
+        probabilities<SCORE, L, R>(z, key_logit<false>(group_max<L>(best)), num, p, sg);
         float gp = 0.0f, chosen = 0.0f, dv = 0.0f, v[R];
 #pragma unroll
         for (int j = 0; j < R; j++) {
@@ -543,50 +555,52 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             }
             dz[j] = !live ? 0.0f : on[j] ? q + w : q;
         }
-        if (t < a.T && a.vecd) {
-            if (e0 < a.E) {
+        if (t >= a.T)
+            continue;
+        const int64_t row = t * a.lddz;
 #pragma unroll
-                for (int j = 0; j < R; j += 4) {
-                    if constexpr (BF16)
-                        *reinterpret_cast<uint2 *>((uint16_t *)a.dz + t * a.lddz + e0 + j) =
-                            make_uint2(pack_bf16x2(dz[j], dz[j + 1]), pack_bf16x2(dz[j + 2], dz[j + 3]));
-                    else
-                        *reinterpret_cast<float4 *>((float *)a.dz + t * a.lddz + e0 + j) =
-                            make_float4(dz[j], dz[j + 1], dz[j + 2], dz[j + 3]);
+        for (int q = 0; q < Q; q++) {
+            const int e = e0 + 4 * L * q, j = 4 * q;
+            if (e + 4 <= a.E) {
+                if constexpr (BF16) {
+                    const uint2 w = make_uint2(pack_bf16x2(dz[j], dz[j + 1]), pack_bf16x2(dz[j + 2], dz[j + 3]));
+                    __builtin_memcpy((uint16_t *)a.dz + row + e, &w, 8);
+                } else {
+                    __builtin_memcpy((float *)a.dz + row + e, &dz[j], 16);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 3; i++)
+                    if (e + i < a.E) {
+                        if constexpr (BF16)
+                            ((__bf16 *)a.dz)[row + e + i] = (__bf16)dz[j + i];
+                        else
+                            ((float *)a.dz)[row + e + i] = dz[j + i];
+                    }
             }
-        } else if (t < a.T) {
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                if (e0 + j < a.E) {
-                    if constexpr (BF16)
-                        ((__bf16 *)a.dz)[t * a.lddz + e0 + j] = (__bf16)dz[j];
-                    else
-                        ((float *)a.dz)[t * a.lddz + e0 + j] = dz[j];
-                }
         }
     }
 }
 
-// Lanes per token.  Forward: a round of the choice costs about 4 R + 35 instructions
-// for 64 / L tokens, so fewer lanes with more experts each are faster (16384 x 256 with
-// the loss: 64 lanes of 4 40 us, 16 of 16 26 us).  Backward: memory and LDS accesses
-// of neighbouring lanes should be neighbours (16384 x 256: 17 us and 38 us).
+// Lanes per token, by what was measured: a round of the choice costs about 10 Q + 20
+// instructions for 64 / L tokens, so fewer lanes with more experts each are faster
+// (forward, 16384 x 256 FP32 with the loss: 16 lanes 24 us, 32 lanes 26 us; 32768 x 512:
+// 32 lanes 51 us, 64 lanes 61 us); the backward pass is level (14.7 and 13.8, 32 and 34).
 static int router_lanes(int E) { return E <= 128 ? 8 : E <= 256 ? 16 : E <= 512 ? 32 : 64; }
-static int router_lanes_bwd(int E) { return E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
 // ... with lane j taking slot j.
 static int at_least_slots(int L, int k)
 {
     const int need = k <= 8 ? 8 : k <= 16 ? 16 : k <= 32 ? 32 : 64;
     return L > need ? L : need;
 }
-static int router_per_lane(int E, int L) { return 4 * L >= E ? 4 : 8 * L >= E && (L == 8 || L == 64) ? 8 : 16; }
 
-// Workgroups of the forward pass, at most four per CU; one alone needs no second launch.
+// Workgroups of the forward pass, at most three per CU (four: 16384 x 256 24 against
+// 22 us, more partial results to add); one alone needs no second launch, and takes the
+// tokens of two in turn in the same time (64 x 32: 6.8 us both ways).
 static int64_t router_blocks(int64_t T, int E)
 {
     const int64_t per = 256 / router_lanes(E), n = (T + per - 1) / per;
-    return n < 1 ? 1 : n < 1024 ? n : 1024;
+    return n < 3 ? 1 : n < 768 ? n : 768;
 }
 
 static int reduce_blocks(int E) { return (E + RED_COLS - 1) / RED_COLS; }
@@ -607,30 +621,24 @@ static int check_router(const char *name, const void *z, int dtype, int64_t T, i
 
 template <bool BF16, int SCORE, bool FWD> static void launch_router(RouterArgs a, hipStream_t st)
 {
-    const int L = at_least_slots(FWD ? router_lanes(a.E) : router_lanes_bwd(a.E), a.k), groups = 256 / L;
-    const int R = router_per_lane(a.E, L);
-    a.vec = a.E % R == 0 && a.ldz % 4 == 0 && ((uintptr_t)a.z & (BF16 ? 7 : 15)) == 0;
-    a.vecd = a.E % R == 0 && a.lddz % 4 == 0 && ((uintptr_t)a.dz & (BF16 ? 7 : 15)) == 0;
+    const int L = at_least_slots(router_lanes(a.E), a.k), groups = 256 / L;
+    const int Q = (a.E + 4 * L - 1) / (4 * L);
     const int64_t n = (a.T + groups - 1) / groups;
     const unsigned grid = (unsigned)(FWD ? router_blocks(a.T, a.E) : n < 2048 ? n : 2048);
-    const size_t lds = FWD ? (size_t)4 * ((a.loss ? groups * a.E : 0) + a.E + 1) : (size_t)4 * 256 * R;
+    const size_t lds = FWD ? (size_t)4 * ((a.loss ? groups * a.E : 0) + a.E + 1) : (size_t)16 * 256 * Q;
 #define FGB_R(LANES, PER)                                                                                              \
-    if (L == LANES && R == PER) {                                                                                      \
+    if (L == LANES && Q == PER) {                                                                                      \
         if constexpr (FWD)                                                                                             \
             router_fwd_kernel<BF16, SCORE, LANES, PER><<<grid, 256, lds, st>>>(a);                                     \
         else                                                                                                           \
             router_bwd_kernel<BF16, SCORE, LANES, PER><<<grid, 256, lds, st>>>(a);                                     \
     }
-    FGB_R(8, 4)
-    FGB_R(8, 8)
-    FGB_R(8, 16)
-    FGB_R(16, 4)
-    FGB_R(16, 16)
-    FGB_R(32, 4)
-    FGB_R(32, 16)
-    FGB_R(64, 4)
-    FGB_R(64, 8)
-    FGB_R(64, 16)
+#define FGB_L(LANES) FGB_R(LANES, 1) FGB_R(LANES, 2) FGB_R(LANES, 3) FGB_R(LANES, 4)
+    FGB_L(8)
+    FGB_L(16)
+    FGB_L(32)
+    FGB_L(64)
+#undef FGB_L
 #undef FGB_R
 }
 

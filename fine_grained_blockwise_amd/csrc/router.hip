@@ -385,93 +385,110 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
     }
 }
 
-// Counts and loss from the workgroups' partial results: 32 experts a workgroup, 32
-// threads to an expert, added in order; the first workgroup takes the live tokens too.
-// Up to 32 experts one workgroup writes the loss; beyond, the one that comes last (the
-// ticket, zeroed by the forward kernel) adds the workgroups' parts, in order too.  One
-// workgroup for all of 257 experts moved its 1 MB (512 partial results) at one CU's
-// rate: 60 us against 7.
-constexpr int RED_COLS = 32, RED_SLICES = 32;
-__global__ __launch_bounds__(RED_COLS * RED_SLICES) void router_reduce_kernel(RouterArgs a, int blocks)
+// Counts and loss from the workgroups' partial results: COLS experts a workgroup, 1024 /
+// COLS threads to an expert, added in a fixed order; the first workgroup takes the live
+// tokens too.  Up to 32 experts one workgroup writes the loss; beyond, the one that comes
+// last (the ticket, zeroed by the forward kernel) adds the workgroups' parts, a lane each,
+// in a fixed order too.  The ticket costs about 2 us, so 32 experts go to one workgroup
+// (512 x 32 with the loss: 7.7 us, two workgroups 9.0 us); beyond, a CU's rate over its
+// columns counts (4999 x 257: 15.8 us with 32 experts each, 15.2 us with 16).
+constexpr int RED_WAVES = 16;
+template <int COLS> __global__ __launch_bounds__(64 * RED_WAVES) void router_reduce_kernel(RouterArgs a, int blocks)
 {
-    __shared__ double fsum[RED_SLICES / 2][RED_COLS];
-    __shared__ int csum[RED_SLICES / 2][RED_COLS], lsum[RED_SLICES / 2];
-    const int col = threadIdx.x % RED_COLS, slice = threadIdx.x / RED_COLS;
-    const int e = blockIdx.x * RED_COLS + col;
+    constexpr int SLICES = 64 * RED_WAVES / COLS;
+    __shared__ double fsum[RED_WAVES][COLS];
+    __shared__ int csum[RED_WAVES][COLS], lsum[RED_WAVES];
+    const int col = threadIdx.x % COLS, slice = threadIdx.x / COLS;
+    const int e = blockIdx.x * COLS + col;
     const bool on = e < a.E;
     const int ec = on ? e : a.E - 1;
     int c = 0, live = 0;
     double f = 0.0;
     // eight partial results in flight at a time: loads without branches, the last one
     // again past the end
-    for (int b0 = slice; b0 < blocks; b0 += 8 * RED_SLICES) {
+    for (int b0 = slice; b0 < blocks; b0 += 8 * SLICES) {
         int ci[8], li[8] = {};
         float fi[8] = {};
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            ci[i] = a.pcnt[(int64_t)min(b0 + i * RED_SLICES, blocks - 1) * (a.E + 1) + ec];
+            ci[i] = a.pcnt[(int64_t)min(b0 + i * SLICES, blocks - 1) * (a.E + 1) + ec];
         if (a.loss) {
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                fi[i] = a.psum[(int64_t)min(b0 + i * RED_SLICES, blocks - 1) * a.E + ec];
+                fi[i] = a.psum[(int64_t)min(b0 + i * SLICES, blocks - 1) * a.E + ec];
         }
         if (blockIdx.x == 0) {
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                li[i] = a.pcnt[(int64_t)min(b0 + i * RED_SLICES, blocks - 1) * (a.E + 1) + a.E];
+                li[i] = a.pcnt[(int64_t)min(b0 + i * SLICES, blocks - 1) * (a.E + 1) + a.E];
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const bool in = b0 + i * RED_SLICES < blocks;
+            const bool in = b0 + i * SLICES < blocks;
             c += in ? ci[i] : 0;
             live += in ? li[i] : 0;
             f += in ? fi[i] : 0.0f;
         }
     }
-    // two slices to a wave, then the waves in order
-    c += __shfl_xor(c, 32);
-    f += __shfl_xor(f, 32);
-    live += __shfl_xor(live, 32);
-    if ((slice & 1) == 0) {
-        csum[slice / 2][col] = c;
-        fsum[slice / 2][col] = f;
+    // a wave's slices, then the waves in order
+#pragma unroll
+    for (int d = COLS; d < 64; d <<= 1) {
+        c += __shfl_xor(c, d);
+        f += __shfl_xor(f, d);
+        live += __shfl_xor(live, d);
+    }
+    if ((threadIdx.x & 63) < COLS) {
+        const int wave = threadIdx.x >> 6;
+        csum[wave][col] = c;
+        fsum[wave][col] = f;
         if (col == 0)
-            lsum[slice / 2] = live;
+            lsum[wave] = live;
     }
     __syncthreads();
-    if (threadIdx.x >= RED_COLS)
+    if (threadIdx.x >= 64)
         return;
     c = live = 0;
     f = 0.0;
 #pragma unroll
-    for (int s = 0; s < RED_SLICES / 2; s++) {
+    for (int s = 0; s < RED_WAVES; s++) {
         c += csum[s][col];
         live += lsum[s];
         f += fsum[s][col];
     }
-    if (on)
+    const int lane = threadIdx.x;
+    const bool mine = on && lane < COLS;
+    if (mine)
         a.counts[e] = c;
-    double part = on ? (double)c * f : 0.0;
+    double part = mine ? (double)c * f : 0.0;
 #pragma unroll
-    for (int d = RED_COLS / 2; d >= 1; d >>= 1)
+    for (int d = COLS / 2; d >= 1; d >>= 1)
         part += __shfl_xor(part, d);
-    if (threadIdx.x != 0)
-        return;
-    if (blockIdx.x == 0)
+    if (lane == 0 && blockIdx.x == 0)
         __hip_atomic_store(&a.counts[a.E], live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (!a.loss)
         return;
     if (gridDim.x == 1) {
-        write_loss(a, part, live);
+        if (lane == 0)
+            write_loss(a, part, live);
         return;
     }
-    __hip_atomic_store(&a.lpart[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1) {
-        double sum = 0.0;
-        for (int i = 0; i < (int)gridDim.x; i++)
-            sum += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        write_loss(a, sum, __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    int before = 0;
+    if (lane == 0) {
+        __hip_atomic_store(&a.lpart[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        before = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
+    if (__builtin_amdgcn_readfirstlane(before) != (int)gridDim.x - 1)
+        return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    double sum = 0.0; // (at most 1024 / 16 workgroups)
+    live = __hip_atomic_load(&a.counts[a.E], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lane < (int)gridDim.x)
+        sum = __hip_atomic_load(&a.lpart[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        sum += __shfl_xor(sum, d);
+    if (lane == 0)
+        write_loss(a, sum, live);
 }
 
 template <bool BF16, int SCORE, int L, int Q>
@@ -603,7 +620,7 @@ static int64_t router_blocks(int64_t T, int E)
     return n < 3 ? 1 : n < 768 ? n : 768;
 }
 
-static int reduce_blocks(int E) { return (E + RED_COLS - 1) / RED_COLS; }
+static int reduce_blocks(int E) { return E <= 32 ? 1 : (E + 15) / 16; }
 
 static int check_router(const char *name, const void *z, int dtype, int64_t T, int E, int64_t ldz, int k, int score)
 {
@@ -695,7 +712,11 @@ extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64
     dispatch_router<true>(a, dtype, score, (hipStream_t)stream);
     FGB_LAUNCHED("router_fwd_kernel");
     if (blocks > 1) {
-        router_reduce_kernel<<<reduce_blocks(E), RED_COLS * RED_SLICES, 0, (hipStream_t)stream>>>(a, (int)blocks);
+        const int n = reduce_blocks(E);
+        if (n == 1)
+            router_reduce_kernel<32><<<n, 64 * RED_WAVES, 0, (hipStream_t)stream>>>(a, (int)blocks);
+        else
+            router_reduce_kernel<16><<<n, 64 * RED_WAVES, 0, (hipStream_t)stream>>>(a, (int)blocks);
         FGB_LAUNCHED("router_reduce_kernel");
     }
     return FGB_OK;

@@ -612,12 +612,11 @@ static int at_least_slots(int L, int k)
 }
 
 // Workgroups of the forward pass, at most three per CU (four: 16384 x 256 24 against
-// 22 us, more partial results to add); one alone needs no second launch, and takes the
-// tokens of two in turn in the same time (64 x 32: 6.8 us both ways).
+// 22 us, more partial results to add); one alone needs no second launch.
 static int64_t router_blocks(int64_t T, int E)
 {
     const int64_t per = 256 / router_lanes(E), n = (T + per - 1) / per;
-    return n < 3 ? 1 : n < 768 ? n : 768;
+    return n < 1 ? 1 : n < 768 ? n : 768;
 }
 
 static int reduce_blocks(int E) { return E <= 32 ? 1 : (E + 15) / 16; }

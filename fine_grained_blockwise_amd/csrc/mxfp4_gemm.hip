@@ -47,10 +47,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *q, int64
                                              __builtin_amdgcn_readfirstlane((int)bytes), BUF_DWORD3);
 }
 
-// (64 rows of an MXFP4 A: held to 256 registers for two waves a SIMD, 256x7168x2048
+// (64 rows of an MXFP4 A, 64 columns: held to 256 registers for two waves a SIMD, 256x7168x2048
 // 17.6 -> 15.7 us; an E4M3 A would spill there.)
 template <bool A8, int MB, int NB, int W, bool OUT_BF16>
-__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(!A8 && MB == 4 ? 2 : 1))) void mx4_narrow_kernel(Mx4Args p, int tiles_n, int chunks)
+__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(!A8 && MB == 4 && NB == 4 ? 2 : 1))) void mx4_narrow_kernel(Mx4Args p, int tiles_n, int chunks)
 {
     __shared__ v4f part[W][MB * NB][64];
     const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
@@ -267,13 +267,16 @@ template <bool A8, int MB, int NB, int W> static void launch_narrow(const Mx4Arg
 // The narrow kernel's tile: the largest of (16 MB rows, 16 NB columns) whose rows are
 // needed and whose workgroups still reach three quarters of the 256 CUs.  For one row
 // of 2048x7168, 28672x8192: (1, 1) 5.7, 32 us, (1, 4) 12, 29 us; 64 rows: (1, 2) 8.7,
-// 91 us, (4, 4) 20, 44 us.
+// 91 us, (4, 4) 20, 44 us, (4, 8) -, 38 us (E4M3 A 76 and 64 us: fewer reads of A, one
+// wave a SIMD).
 template <bool A8> static void launch_narrow_for(const Mx4Args &p, int64_t blocks, bool bf16, hipStream_t st)
 {
     auto fills = [&](int MB, int NB) {
         return (p.N + 16 * NB - 1) / (16 * NB) * (p.offs ? p.G : (blocks + MB - 1) / MB) >= 192;
     };
-    if (blocks > 2 && fills(4, 4))
+    if (blocks > 2 && fills(4, 8))
+        launch_narrow<A8, 4, 8, 4>(p, bf16, st);
+    else if (blocks > 2 && fills(4, 4))
         launch_narrow<A8, 4, 4, 4>(p, bf16, st);
     else if (blocks > 1 && fills(2, 4))
         launch_narrow<A8, 2, 4, 4>(p, bf16, st);
@@ -321,19 +324,23 @@ template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16
 // tiles 256 at a time, each round 8 us and 1.25 us a 256-element step (1.9 us a
 // 128-element step with an E4M3 A), 1.4 times that where every tile reads other
 // weights (experts of few rows); the narrow one reads the weights once per 16-64 rows
-// and reaches 0.65 (0.38) PFLOP/s, less only where it is bound by bytes and far ahead.
-// Measured, narrow against tiled, MXFP4 A: 512x2048x7168 20 / 42 us, 1024x2048x7168
-// 38 / 42, 256x7168x2048 18.5 / 18.1, 64x28672x8192 44 / 53, 128x28672x8192 84 / 53, 32
-// experts of 16 rows (4096x7168) 106 / 122; E4M3 A: 1024x2048x7168 62 / 115,
-// 256x7168x2048 28 / 38, 512x7168x2048 53 / 39, 64x28672x8192 75 / 133, 256x28672x8192
-// 255 / 134, 32 experts of 48 rows 248 / 324.
+// and reaches 0.78 (0.55) PFLOP/s, less only where it is bound by bytes and far ahead;
+// its 64 x 128 blocks of a dense product of more than 64 rows run 256 at a time too.
+// Measured, narrow against tiled, MXFP4 A: 512x2048x7168 19 / 42 us, 1024x2048x7168
+// 28 / 42, 256x7168x2048 14.5 / 18, 320x7168x2048 26 / 18.6, 64x28672x8192 40 / 56,
+// 128x28672x8192 63 / 53, 32 experts of 32 rows (4096x7168) 114 / 131; E4M3 A:
+// 1024x2048x7168 53 / 115, 256x7168x2048 21 / 38, 768x7168x2048 59 / 39, 128x28672x8192
+// 112 / 133, 192x28672x8192 163 / 134, 32 experts of 64 rows 221 / 331, of 128 417 / 339.
 static bool takes_narrow(const Mx4Args &p, int a_fmt)
 {
     const bool a8 = a_fmt == FGB_E4M3;
     const double step_us = a8 ? (double)(p.K / 128) * 1.9 : (double)((p.K + 255) / 256) * 1.25;
     const double tile_us = (8.0 + step_us) * (p.offs ? 1.4 : 1.0);
     const int64_t tiles = ((p.M + 255) / 256 + (p.offs ? p.G / 2 : 0)) * ((p.N + 255) / 256);
-    const double narrow_us = 2e-9 * (double)p.M * (double)p.N * (double)p.K / (a8 ? 0.38 : 0.65);
+    double work = (double)p.M * (double)p.N;
+    if (!p.offs && p.M > 64)
+        work = (double)(((p.M + 63) / 64 * ((p.N + 127) / 128) + 255) / 256 * 256) * (64 * 128);
+    const double narrow_us = 2e-9 * work * (double)p.K / (a8 ? 0.55 : 0.78);
     return narrow_us <= tile_us * (double)((tiles + 255) / 256);
 }
 

@@ -281,6 +281,23 @@ def test_grouped_gemm(rows, N, K, fmt):
             check_product(f[lo:hi], av[lo:hi], ws[g][2])
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(50, 24600, 384), (64, 24576, 128), (201, 7170, 640)])
+def test_gemm_wide_blocks(M, N, K, fmt):
+    """Many columns at 33 rows or more: 64 x 128 blocks, with odd rows, columns and K."""
+    say("gemm", M, N, K, fmt)
+    a, sa, av = operand_a(M, K, fmt, 5)
+    b, sb, bv = operand_b(N, K, 6)
+    check_product(fgb().mxfp4_gemm(a, sa, b, sb, a_fmt=FMT[fmt], out_dtype=torch.float32), av, bv)
+    check_product(fgb().mxfp4_gemm(a, sa, b, sb, a_fmt=FMT[fmt]), av, bv)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_grouped_gemm_wide_blocks(fmt):
+    """As many experts as make 64 x 128 blocks of few columns, of 0 to 130 rows."""
+    test_grouped_gemm([0, 48, 64, 65, 130, 16, 1, 63] * 8, 400, 384, fmt)
+
+
 def test_other_streams():
     """Calls on a side stream, ordered after the tensors' own: the same bits."""
     x, w = values(200, 512, 1, torch.bfloat16).to(DEV), values(300, 512, 2, torch.bfloat16).to(DEV)

@@ -31,6 +31,11 @@ struct Mx4Args {
 // ends with four consecutive columns of one row of D.  The next unit's loads are
 // issued before a unit is multiplied.  One token's eight experts (4096x7168, E4M3 A,
 // 125 MB): 30 us, 4.2 TB/s; 28672x8192: 29 us, 4.3 TB/s with 4 us of launch in it.
+//
+// Buffer loads: what lies past an operand's last row reads as zeros.  The range check
+// holds the lane's offset alone against the record count, so a row block's and unit's
+// offset goes into the descriptor (scalar instructions; in the lanes' offsets it took
+// 4 to 24 registers and spilled 18), never into the load's scalar offset.
 template <bool A8, int MB, int NB> struct NarrowUnit {
     uint4 b[NB][2], a[MB][A8 ? 4 : 2];
     uint2 bs[NB], as[MB]; // scale bytes of a row: all eight groups (an E4M3 A: .x holds its two)
@@ -45,6 +50,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t *q, int64
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
     return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)(((uint64_t)hi << 32) | lo), 0,
                                              __builtin_amdgcn_readfirstlane((int)bytes), BUF_DWORD3);
+}
+
+// The same from byte `skip` of the `bytes` on: nothing where that is past them.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_from(const uint8_t *q, int bytes, int skip)
+{
+    return buffer(q + skip, max(bytes - skip, 0));
 }
 
 // (64 rows of an MXFP4 A, 64 columns: held to 256 registers for two waves a SIMD, 256x7168x2048
@@ -93,19 +104,18 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(!A8 && M
             sb += (int64_t)e * p.N * units * 8;
         }
         const int64_t n0 = (int64_t)tn * (16 * NB);
-        // Buffer loads: one offset register serves a lane's rows, and what lies past an
-        // operand's last row reads as zeros.
         b += n0 * p.ldb;
         sb += n0 * 8;
         const int bn = (int)min((int64_t)(16 * NB), p.N - n0);
-        const auto brs = buffer(b, (bn - 1) * p.ldb + p.K / 2);
+        const int bbytes = (int)((bn - 1) * p.ldb + p.K / 2), bblock = (int)(16 * p.ldb);
         const uint32_t boff = (uint32_t)(r * p.ldb + h * 16);
         for (int64_t m0 = lo + (int64_t)chunk * (16 * MB); m0 < hi; m0 += (int64_t)chunks * (16 * MB)) {
             const int am = (int)min((int64_t)(16 * MB), hi - m0);
-            const auto ars = buffer(p.a + m0 * p.lda, (am - 1) * p.lda + (A8 ? p.K : p.K / 2));
+            const uint8_t *const a = p.a + m0 * p.lda;
+            const int abytes = (int)((am - 1) * p.lda + (A8 ? p.K : p.K / 2)), ablock = (int)(16 * p.lda);
             const uint32_t aoff = (uint32_t)(r * p.lda + h * (A8 ? 32 : 16));
-            const int64_t as_row = p.K / 128; // E4M3 A: its scales, row-major
-            const auto asrs8 = buffer(p.sa + m0 * as_row, am * as_row);
+            const int as_row = (int)(p.K / 128); // E4M3 A: its scales, row-major
+            const uint8_t *const sa8 = p.sa + m0 * as_row;
             v4f acc[MB][NB];
 #pragma unroll
             for (int i = 0; i < MB; i++)
@@ -118,30 +128,30 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(!A8 && M
                 const auto bsrs = buffer(sb + (int64_t)u * p.N * 8, bn * 8);
 #pragma unroll
                 for (int j = 0; j < NB; j++) {
-                    const uint32_t at = (uint32_t)(j * 16 * p.ldb) + (uint32_t)u * 128;
-                    x.b[j][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff, at, 0));
-                    x.b[j][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff + 64, at, 0));
+                    const auto brs = buffer_from(b, bbytes, j * bblock + u * 128);
+                    x.b[j][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff, 0, 0));
+                    x.b[j][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(brs, boff + 64, 0, 0));
                     x.bs[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bsrs, r * 8 + j * 128, 0, 0));
                 }
                 if constexpr (A8) {
 #pragma unroll
                     for (int i = 0; i < MB; i++) {
-                        const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 256;
+                        const auto ars = buffer_from(a, abytes, i * ablock + u * 256);
 #pragma unroll
                         for (int k = 0; k < 4; k++)
                             x.a[i][k] = __builtin_bit_cast(
-                                uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + (k / 2) * 128 + (k & 1) * 16, at, 0));
-                        const uint32_t row = (uint32_t)((i * 16 + r) * as_row);
-                        x.as[i].x = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row, 2 * u, 0);
-                        x.as[i].y = __builtin_amdgcn_raw_buffer_load_b8(asrs8, row + 1, 2 * u, 0);
+                                uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + (k / 2) * 128 + (k & 1) * 16, 0, 0));
+                        const auto asrs = buffer_from(sa8, am * as_row, i * 16 * as_row + 2 * u);
+                        x.as[i].x = __builtin_amdgcn_raw_buffer_load_b8(asrs, r * as_row, 0, 0);
+                        x.as[i].y = __builtin_amdgcn_raw_buffer_load_b8(asrs, r * as_row + 1, 0, 0);
                     }
                 } else {
                     const auto asrs = buffer(p.sa + ((int64_t)u * p.M + m0) * 8, am * 8);
 #pragma unroll
                     for (int i = 0; i < MB; i++) {
-                        const uint32_t at = (uint32_t)(i * 16 * p.lda) + (uint32_t)u * 128;
-                        x.a[i][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff, at, 0));
-                        x.a[i][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + 64, at, 0));
+                        const auto ars = buffer_from(a, abytes, i * ablock + u * 128);
+                        x.a[i][0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff, 0, 0));
+                        x.a[i][1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(ars, aoff + 64, 0, 0));
                         x.as[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(asrs, r * 8 + i * 128, 0, 0));
                     }
                 }

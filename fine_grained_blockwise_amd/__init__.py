@@ -185,7 +185,12 @@ def _check_dev(*ts):
 def _row_ld(t):
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    return t.stride(0)
+    return _ld(t)
+
+
+def _ld(t):
+    # torch may hold any number as the stride of a single row: it is not looked at
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _need(t, name, shape=None, dtype=None, contiguous=False):
@@ -926,11 +931,12 @@ def _mxfp4_input(x, name):
         raise ValueError(f"{name}: cols ({cols}) must be a multiple of 32")
     _check_dev(x)
     # anything but aligned rows of unit stride (stacked without gaps) is copied once
-    st = x.stride()
-    if (st[-1] != 1 or st[-2] < cols or st[-2] * x.element_size() % 16 or x.data_ptr() % 16
-            or (len(shape) == 3 and st[0] != rows * st[-2])):
-        x = x.contiguous() if not x.is_contiguous() else x.clone()
-    return x, tuple(shape[:-2]), rows, cols
+    st, G = x.stride(), shape[0] if len(shape) == 3 else 1
+    ld = st[-2] if rows > 1 else st[0] if G > 1 else cols  # (a single row's or matrix's stride means nothing)
+    if (st[-1] != 1 or ld < cols or ld * x.element_size() % 16 or x.data_ptr() % 16
+            or (G > 1 and st[0] != rows * ld)):
+        x, ld = x.clone(memory_format=torch.contiguous_format), cols
+    return x, tuple(shape[:-2]), rows, cols, ld
 
 
 def _mxfp4_out(lead, rows, cols, dev):
@@ -943,9 +949,9 @@ def mxfp4_quant(x, rule=SCALE_CEIL):
     """MXFP4 quantization of x [rows, cols] (fp32/bf16, cols % 32 == 0) -> (q uint8 [rows, cols/2],
     s uint8 [ceil(cols/256), rows, 8]), or of stacked matrices x [G, rows, cols] -> (q [G, ...], s [G, ...]);
     see include/fgb.h for the layouts."""
-    x, lead, rows, cols = _mxfp4_input(x, "mxfp4_quant")
+    x, lead, rows, cols, ld = _mxfp4_input(x, "mxfp4_quant")
     q, s = _mxfp4_out(lead, rows, cols, x.device)
-    _call("mxfp4_quant", x.data_ptr(), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule,
+    _call("mxfp4_quant", x.data_ptr(), _dtype_code(x), lead[0] if lead else 1, rows, cols, ld, rule,
           q.data_ptr(), s.data_ptr(), _stream(x))
     return q, s
 
@@ -954,10 +960,10 @@ def mxfp4_quant_t(x, rule=SCALE_CEIL):
     """MXFP4 quantization of x [rows, cols] (or [G, rows, cols]) and of its transpose, in one pass:
     -> (q, s, qt, st), qt and st being those of a [cols, R] tensor, R = rows rounded up to 32 (columns past rows
     are zeros)."""
-    x, lead, rows, cols = _mxfp4_input(x, "mxfp4_quant_t")
+    x, lead, rows, cols, ld = _mxfp4_input(x, "mxfp4_quant_t")
     q, s = _mxfp4_out(lead, rows, cols, x.device)
     qt, st = _mxfp4_out(lead, cols, (rows + 31) // 32 * 32, x.device)
-    _call("mxfp4_quant_t", x.data_ptr(), _dtype_code(x), lead[0] if lead else 1, rows, cols, x.stride(-2), rule,
+    _call("mxfp4_quant_t", x.data_ptr(), _dtype_code(x), lead[0] if lead else 1, rows, cols, ld, rule,
           q.data_ptr(), s.data_ptr(), qt.data_ptr(), st.data_ptr(), _stream(x))
     return q, s, qt, st
 
@@ -1071,7 +1077,7 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
     weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
     counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef else None
-    _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(token_mask), score, int(bool(renorm)), scale,
+    _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), score, int(bool(renorm)), scale,
           loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(workspace),
           0 if workspace is None else workspace.numel(), _stream(logits))
     return idx, weights, counts, loss
@@ -1096,6 +1102,6 @@ def moe_router_backward(logits, topk_idx, counts, dweights=None, dloss=None, sco
             raise ValueError(f"{name}: dloss must hold one value")
     _check_dev(logits, topk_idx, counts, dweights, dloss)
     dz = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
-    _call(name, _ptr(logits), dt, T, E, logits.stride(0), topk, _ptr(topk_idx), _ptr(counts), _ptr(dweights),
+    _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(topk_idx), _ptr(counts), _ptr(dweights),
           _ptr(dloss), score, int(bool(renorm)), scale, loss_coef, _ptr(dz), E, _stream(logits))
     return dz

@@ -1,0 +1,70 @@
+"""Calls of the MXFP4 and router entry points that differ from the usual in how their tensors lie in memory or in
+how many there are: the same results as the usual calls, bit for bit."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def fgb():
+    import fine_grained_blockwise_amd as m
+    return m
+
+
+def randn(*shape, seed=0, dtype=torch.bfloat16):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype).to(DEV)
+
+
+def equal(a, b):
+    return all((x is None and y is None) or torch.equal(x, y) for x, y in zip(a, b))
+
+
+def single_row(x):
+    """x [1, n] as the transpose of a column: torch calls it contiguous and its strides are (1, 1)."""
+    t = x.t().clone(memory_format=torch.contiguous_format).t()
+    assert t.stride() == (1, 1) and t.is_contiguous() and torch.equal(t, x)
+    return t
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_single_row_of_any_row_stride(dtype):
+    m = fgb()
+    z = randn(1, 40, dtype=dtype)
+    for lg in (single_row(z), torch.cat([z] * 3, 1)[:, 40:80]):
+        want, got = (m.moe_router(t, 4, renorm=True, loss_coef=0.1) for t in (z, lg))
+        assert equal(want, got)
+        w = torch.ones((1, 4), device=DEV)
+        assert torch.equal(m.moe_router_backward(z, want[0], want[2], w), m.moe_router_backward(lg, got[0], got[2], w))
+    x = randn(1, 96, seed=1, dtype=dtype)
+    stacked = torch.empty_strided((3, 1, 96), (96, 1, 1), dtype=dtype, device=DEV)
+    stacked.copy_(randn(3, 1, 96, seed=2, dtype=dtype))
+    apart = randn(3, 2, 96, seed=3, dtype=dtype)[:, :1]
+    for quant in (m.mxfp4_quant, m.mxfp4_quant_t):
+        assert equal(quant(x), quant(single_row(x)))
+        assert equal(quant(stacked.clone(memory_format=torch.contiguous_format)), quant(stacked))
+        assert equal(quant(apart.contiguous()), quant(apart))
+    empty = torch.empty((40, 0), dtype=dtype, device=DEV).t()
+    assert m.moe_router(empty, 4)[0].shape == (0, 4)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_a_single_row_in_a_product(fmt):
+    m = fgb()
+    x, (b, sb) = randn(1, 256), m.mxfp4_quant(randn(16, 256, seed=1))
+    a, sa = m.mxfp4_quant(x) if fmt == "e2m1" else m.fp8_quant_rowwise(x)
+    f = m.E2M1 if fmt == "e2m1" else m.E4M3
+    want = m.mxfp4_gemm(a, sa, b, sb, a_fmt=f)
+    d = single_row(torch.zeros_like(want))
+    assert m.mxfp4_gemm(single_row(a), sa, b, sb, a_fmt=f, d=d) is d
+    assert torch.equal(want, d)
+
+
+def test_a_single_row_in_the_fp8_calls():
+    m = fgb()
+    x, w = randn(1, 256), randn(128, 256, seed=1)
+    xq, xs = m.fp8_quant_rowwise(x)
+    assert equal((xq, xs), m.fp8_quant_rowwise(single_row(x)))
+    wq, ws = m.fp8_quant_blockwise(w)
+    assert torch.equal(m.fp8_block_gemm(xq, xs, m.ROW1x128, wq, ws, m.BLOCK128),
+                       m.fp8_block_gemm(single_row(xq), xs, m.ROW1x128, wq, ws, m.BLOCK128))

@@ -984,6 +984,11 @@ def mxfp4_dequant(q, s, out_dtype=torch.float32):
     return out
 
 
+def _mxfp4_sa(sa, a_fmt):
+    # (one slice of stacked MXFP4 scales may start at a multiple of 8: copied)
+    return sa.clone() if a_fmt == E2M1 and sa.data_ptr() % 16 else sa
+
+
 def _mxfp4_a(a, a_fmt, name):
     """M and K of the A operand, and the shape of its scales."""
     if a_fmt not in (E2M1, E4M3):
@@ -1014,6 +1019,7 @@ def mxfp4_gemm(a, sa, b, sb, a_fmt=E2M1, out_dtype=torch.bfloat16, d=None, accum
     _check_dev(a, sa, b, sb, d)
     if d is None:
         d = torch.empty(M, N, dtype=out_dtype, device=a.device)
+    sa = _mxfp4_sa(sa, a_fmt)
     _call(name, a.data_ptr(), sa.data_ptr(), a_fmt, b.data_ptr(), sb.data_ptr(), M, N, K, _row_ld(a), _row_ld(b),
           d.data_ptr(), _dtype_code(d), _row_ld(d), 1 if accumulate else 0, _stream(a))
     return d
@@ -1036,6 +1042,7 @@ def mxfp4_grouped_gemm(a, sa, b, sb, group_offsets, a_fmt=E4M3, out_dtype=torch.
     _check_dev(a, sa, b, sb, group_offsets, d)
     if d is None:
         d = torch.empty(M_cap, N, dtype=out_dtype, device=a.device)
+    sa = _mxfp4_sa(sa, a_fmt)
     _call(name, a.data_ptr(), sa.data_ptr(), a_fmt, b.data_ptr(), sb.data_ptr(), group_offsets.data_ptr(), G, M_cap, N,
           K, d.data_ptr(), _dtype_code(d), _stream(a))
     return d

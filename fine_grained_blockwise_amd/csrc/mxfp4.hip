@@ -491,8 +491,7 @@ extern "C" int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, i
     if (rows == 0 || cols == 0)
         return FGB_OK;
     FGB_REQUIRE(q && s && out, FGB_EINVAL, "mxfp4_dequant: null pointer");
-    FGB_REQUIRE(aligned16(q) && aligned16(s) && aligned16(out), FGB_EINVAL,
-                "mxfp4_dequant: q, s and out must be 16-byte aligned");
+    FGB_REQUIRE(aligned16(q) && aligned16(out), FGB_EINVAL, "mxfp4_dequant: q and out must be 16-byte aligned");
     FGB_REQUIRE(rows < (1ll << 31) && cols < (1ll << 31) && rows * (cols / 32) < (1ll << 33), FGB_EINVAL,
                 "mxfp4_dequant: too many elements");
     const int64_t grid = (rows * cols / 8 + 255) / 256;

@@ -311,6 +311,17 @@ static int check_mx4(const char *name, int a_fmt, int64_t M, int64_t N, int64_t 
     return FGB_OK;
 }
 
+// (Weights' scales are read in pieces of 8 bytes a row, whose runs start at any row: an
+// expert's slice of a stack with odd rows and steps starts at a multiple of 8.)
+static int check_aligned(const char *name, const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b,
+                         const uint8_t *sb, int64_t K)
+{
+    FGB_REQUIRE(K == 0 || (aligned16(a) && aligned16(b) && ((uintptr_t)sb & 7) == 0 &&
+                           (a_fmt == FGB_E4M3 || aligned16(sa))),
+                FGB_EINVAL, "%s: a, b and an MXFP4 A's scales must be 16-byte aligned, B's scales 8-byte", name);
+    return FGB_OK;
+}
+
 // The 256 x 256-tiled kernel of gemm_kernel.h.
 template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16, hipStream_t st)
 {
@@ -395,8 +406,9 @@ extern "C" int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const 
     FGB_REQUIRE(ldd >= N, FGB_EINVAL, "mxfp4_gemm: ldd must be >= N");
     FGB_REQUIRE(d_dtype == FGB_BF16 || ldd < (1ll << 23), FGB_EUNSUPPORTED,
                 "mxfp4_gemm: FP32 output rows (ldd) must be shorter than 2^23 elements");
-    FGB_REQUIRE(K == 0 || (aligned16(a) && aligned16(b) && aligned16(sb) && (a_fmt == FGB_E4M3 || aligned16(sa))),
-                FGB_EINVAL, "mxfp4_gemm: a, b and their 1x32 scales must be 16-byte aligned");
+    const int rc_align = check_aligned("mxfp4_gemm", a, sa, a_fmt, b, sb, K);
+    if (rc_align != FGB_OK)
+        return rc_align;
     FGB_REQUIRE(((uintptr_t)d & (d_dtype == FGB_BF16 ? 1 : 3)) == 0, FGB_EINVAL, "mxfp4_gemm: d misaligned");
     Mx4Args p{};
     p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d;
@@ -420,8 +432,9 @@ extern "C" int mxfp4_grouped_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt
     FGB_REQUIRE(d_dtype == FGB_BF16 || N < (1ll << 23), FGB_EUNSUPPORTED,
                 "mxfp4_grouped_gemm: FP32 output rows must be shorter than 2^23 elements");
     FGB_REQUIRE(d && group_offsets && (K == 0 || (a && sa && b && sb)), FGB_EINVAL, "mxfp4_grouped_gemm: null pointer");
-    FGB_REQUIRE(K == 0 || (aligned16(a) && aligned16(b) && aligned16(sb) && (a_fmt == FGB_E4M3 || aligned16(sa))),
-                FGB_EINVAL, "mxfp4_grouped_gemm: a, b and their 1x32 scales must be 16-byte aligned");
+    const int rc_align = check_aligned("mxfp4_grouped_gemm", a, sa, a_fmt, b, sb, K);
+    if (rc_align != FGB_OK)
+        return rc_align;
     FGB_REQUIRE(((uintptr_t)d & (d_dtype == FGB_BF16 ? 1 : 3)) == 0 && ((uintptr_t)group_offsets & 3) == 0, FGB_EINVAL,
                 "mxfp4_grouped_gemm: d or group_offsets misaligned");
     Mx4Args p{};

@@ -615,7 +615,8 @@ int mxfp4_quant(const void *x, int x_dtype, int G, int64_t rows, int64_t cols, i
 int mxfp4_quant_t(const void *x, int x_dtype, int G, int64_t rows, int64_t cols, int64_t ldx, int rule, uint8_t *q,
                   uint8_t *s, uint8_t *qt, uint8_t *st, void *stream);
 
-/* mxfp4_dequant -- decode(q) * 2^(s - 127) into out [rows, cols] dense, FP32 or BF16 (nearest even). */
+/* mxfp4_dequant -- decode(q) * 2^(s - 127) into out [rows, cols] dense, FP32 or BF16 (nearest even); q and out
+ * 16-byte aligned. */
 int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols, void *out, int out_dtype,
                   void *stream);
 
@@ -630,8 +631,9 @@ int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols
  *                  FP32 output needs ldd < 2^23 (else FGB_EUNSUPPORTED);
  *                  accumulate != 0 (FP32 only): D += A * B^T.
  * M, N >= 0 (0: nothing is written); K = 0: D = 0 (or unchanged when
- * accumulating).  lda and ldb multiples of 16 below 2^23; a, b, sb and an MXFP4
- * sa 16-byte aligned, an E4M3 A's scales and D at their element's size.  With an
+ * accumulating).  lda and ldb multiples of 16 below 2^23; a, b and an MXFP4 sa
+ * 16-byte aligned, sb 8-byte (an expert's slice of a stack), an E4M3 A's scales and
+ * D at their element's size.  With an
  * E4M3 A each code times its scale becomes a bf16 (exact wherever the value has a
  * bf16 representation) and products are exact; with an MXFP4 A the matrix unit
  * takes codes and scales, its sums measured at FP32 rounding.  Results do not

@@ -68,3 +68,23 @@ def test_a_single_row_in_the_fp8_calls():
     wq, ws = m.fp8_quant_blockwise(w)
     assert torch.equal(m.fp8_block_gemm(xq, xs, m.ROW1x128, wq, ws, m.BLOCK128),
                        m.fp8_block_gemm(single_row(xq), xs, m.ROW1x128, wq, ws, m.BLOCK128))
+
+
+def test_slices_of_stacked_scales():
+    """Scales of 5 rows and one step take 40 bytes: the odd slices of a stack start at a multiple of 8 only."""
+    m = fgb()
+    q, s = m.mxfp4_quant(randn(4, 5, 160))
+    xq, xs = m.mxfp4_quant(randn(4, 5, 160, seed=1))
+    x8, x8s = m.fp8_quant_rowwise(randn(5, 256, seed=2))
+    w8, w8s = m.mxfp4_quant(randn(4, 5, 256, seed=3))
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device=DEV)
+    for i in range(4):
+        assert s[i].data_ptr() % 16 == 8 * (i % 2) and s[i].is_contiguous()
+        whole = [t[i].clone() for t in (q, s, xq, xs, w8, w8s)]
+        assert torch.equal(m.mxfp4_dequant(q[i], s[i]), m.mxfp4_dequant(*whole[:2]))
+        assert torch.equal(m.mxfp4_gemm(xq[i], xs[i], q[i], s[i]), m.mxfp4_gemm(*whole[2:4], *whole[:2]))
+        assert torch.equal(m.mxfp4_gemm(x8, x8s, w8[i], w8s[i], a_fmt=m.E4M3),
+                           m.mxfp4_gemm(x8, x8s, *whole[4:], a_fmt=m.E4M3))
+    got = m.mxfp4_grouped_gemm(xq[1], xs[1], q[1:3], s[1:3], off, a_fmt=m.E2M1)
+    want = m.mxfp4_grouped_gemm(xq[1].clone(), xs[1].clone(), q[1:3].clone(), s[1:3].clone(), off, a_fmt=m.E2M1)
+    assert torch.equal(got, want)

@@ -133,10 +133,10 @@ __device__ __forceinline__ uint32_t four_bytes(uint32_t b)
 // 2 (4) bytes read and 17/32 written per element.  8192x28672 bf16: 103 us, 5.8 TB/s.
 template <bool BF16, int RULE>
 __global__ __launch_bounds__(256) void mxfp4_quant_kernel(const void *x, int64_t rows, int64_t cols, int64_t ldx,
-                                                          uint8_t *q, uint8_t *s, int steps, int tiles_m)
+                                                          uint8_t *q, uint8_t *s, int steps, int tiles_m, int first)
 {
     constexpr int U = 4;
-    const int step = blockIdx.x % steps, tile = blockIdx.x / steps, z = tile / tiles_m;
+    const int step = blockIdx.x % steps, tile = first + blockIdx.x / steps, z = tile / tiles_m;
     const int64_t row0 = (int64_t)(tile % tiles_m) * (8 * U) + (threadIdx.x >> 5);
     const int64_t col = (int64_t)step * 256 + (threadIdx.x & 31) * 8;
     x = (const uint8_t *)x + z * rows * ldx * (BF16 ? 2 : 4);
@@ -372,9 +372,9 @@ __global__ __launch_bounds__(512) void mxfp4_quant_t_f32_kernel(const void *x, i
 // Eight codes per lane.
 template <bool BF16>
 __global__ __launch_bounds__(256) void mxfp4_dequant_kernel(const uint8_t *q, const uint8_t *s, int64_t rows,
-                                                            int64_t cols, void *out)
+                                                            int64_t cols, void *out, int64_t first)
 {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int64_t at = ((first + blockIdx.x) * 256 + threadIdx.x) * 8;
     if (at >= rows * cols)
         return;
     const int64_t row = at / cols, col = at % cols;
@@ -397,6 +397,10 @@ __global__ __launch_bounds__(256) void mxfp4_dequant_kernel(const uint8_t *q, co
         o[1] = make_float4(c[0], c[1], d[0], d[1]);
     }
 }
+
+// Workgroups of one launch: the runtime keeps the low 32 bits of a launch's threads, without
+// an error, so larger work goes in several launches (256 threads each: 2^31 threads).
+constexpr int64_t LAUNCH_BLOCKS = 1 << 23;
 
 static int check_quant(const char *name, const void *x, int x_dtype, int G, int64_t rows, int64_t cols, int64_t ldx, int rule,
                        const void *q, const void *s)
@@ -440,11 +444,14 @@ extern "C" int mxfp4_quant(const void *x, int x_dtype, int G, int64_t rows, int6
     const int rc = check_quant("mxfp4_quant", x, x_dtype, G, rows, cols, ldx, rule, q, s);
     if (rc != FGB_OK || G == 0 || rows == 0 || cols == 0)
         return rc;
-    const int64_t steps = (cols + 255) / 256, tiles_m = (rows + 31) / 32;
-    const int64_t grid = steps * tiles_m * G;
-    FGB_BY_TYPE_AND_RULE(mxfp4_quant_kernel, <<<(unsigned)grid, 256, 0, (hipStream_t)stream>>>(
-                                                 x, rows, cols, ldx, q, s, (int)steps, (int)tiles_m));
-    FGB_LAUNCHED("mxfp4_quant_kernel");
+    const int64_t steps = (cols + 255) / 256, tiles_m = (rows + 31) / 32, tiles = tiles_m * G;
+    const int64_t most = steps < LAUNCH_BLOCKS ? LAUNCH_BLOCKS / steps : 1; // tiles of a launch
+    for (int64_t first = 0; first < tiles; first += most) {
+        const int64_t grid = steps * (tiles - first < most ? tiles - first : most);
+        FGB_BY_TYPE_AND_RULE(mxfp4_quant_kernel, <<<(unsigned)grid, 256, 0, (hipStream_t)stream>>>(
+                                                     x, rows, cols, ldx, q, s, (int)steps, (int)tiles_m, (int)first));
+        FGB_LAUNCHED("mxfp4_quant_kernel");
+    }
     return FGB_OK;
 }
 
@@ -470,6 +477,7 @@ extern "C" int mxfp4_quant_t(const void *x, int x_dtype, int G, int64_t rows, in
             mxfp4_quant_t_bf16_kernel<RULE_OCP_FLOOR><<<(unsigned)grid, 512, 0, hs>>>(x, rows, cols, ldx, q, s, qt, st,
                                                                                      (int)tiles_n, (int)tiles_m, (int)tiles);
     } else {
+        FGB_REQUIRE(cols <= (1ll << 30) - 256, FGB_EINVAL, "mxfp4_quant_t: cols of an FP32 x must be below 2^30 - 255");
         const dim3 grid((unsigned)((cols + QT - 1) / QT), (unsigned)gy, (unsigned)G);
         if (rule == FGB_SCALE_CEIL)
             mxfp4_quant_t_f32_kernel<RULE_CEIL><<<grid, 512, 0, hs>>>(x, rows, cols, ldx, q, s, qt, st);
@@ -494,11 +502,14 @@ extern "C" int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, i
     FGB_REQUIRE(aligned16(q) && aligned16(out), FGB_EINVAL, "mxfp4_dequant: q and out must be 16-byte aligned");
     FGB_REQUIRE(rows < (1ll << 31) && cols < (1ll << 31) && rows * (cols / 32) < (1ll << 33), FGB_EINVAL,
                 "mxfp4_dequant: too many elements");
-    const int64_t grid = (rows * cols / 8 + 255) / 256;
-    if (out_dtype == FGB_BF16)
-        mxfp4_dequant_kernel<true><<<(unsigned)grid, 256, 0, (hipStream_t)stream>>>(q, s, rows, cols, out);
-    else
-        mxfp4_dequant_kernel<false><<<(unsigned)grid, 256, 0, (hipStream_t)stream>>>(q, s, rows, cols, out);
-    FGB_LAUNCHED("mxfp4_dequant_kernel");
+    const int64_t blocks = (rows * cols / 8 + 255) / 256;
+    for (int64_t first = 0; first < blocks; first += LAUNCH_BLOCKS) {
+        const unsigned grid = (unsigned)(blocks - first < LAUNCH_BLOCKS ? blocks - first : LAUNCH_BLOCKS);
+        if (out_dtype == FGB_BF16)
+            mxfp4_dequant_kernel<true><<<grid, 256, 0, (hipStream_t)stream>>>(q, s, rows, cols, out, first);
+        else
+            mxfp4_dequant_kernel<false><<<grid, 256, 0, (hipStream_t)stream>>>(q, s, rows, cols, out, first);
+        FGB_LAUNCHED("mxfp4_dequant_kernel");
+    }
     return FGB_OK;
 }

@@ -265,9 +265,11 @@ template <bool A8, int MB, int NB, int W> static void launch_narrow(const Mx4Arg
 {
     const int tiles_n = (int)((p.N + 16 * NB - 1) / (16 * NB));
     const int64_t all = (p.M + 16 * MB - 1) / (16 * MB);
-    const int chunks = p.offs ? 1 : (int)(all < 64 ? all : 64); // (experts' rows: a workgroup takes all)
-    const int64_t pairs = (int64_t)tiles_n * p.G;
-    const int64_t grid = p.offs ? (pairs < 512 ? pairs : 512) : (int64_t)((tiles_n + 7) / 8) * 8 * chunks;
+    const int64_t pairs = (int64_t)tiles_n * p.G, tiles = (int64_t)((tiles_n + 7) / 8) * 8;
+    // (experts' rows: a workgroup takes all; the runtime keeps the low 32 bits of a launch's threads)
+    const int64_t most = (1ll << 31) / (W * 64) / tiles, cap = most < 1 ? 1 : most < 64 ? most : 64;
+    const int chunks = p.offs ? 1 : (int)(all < cap ? all : cap);
+    const int64_t grid = p.offs ? (pairs < 512 ? pairs : 512) : tiles * chunks;
     if (bf16)
         mx4_narrow_kernel<A8, MB, NB, W, true><<<(unsigned)grid, W * 64, 0, st>>>(p, tiles_n, chunks);
     else
@@ -304,8 +306,8 @@ static int check_mx4(const char *name, int a_fmt, int64_t M, int64_t N, int64_t 
     FGB_REQUIRE(M >= 0 && N >= 0 && K >= 0 && K % (a_fmt == FGB_E4M3 ? 128 : 32) == 0, FGB_EINVAL,
                 "%s: need M, N >= 0 and K a multiple of 32 (128 with an E4M3 A) (M=%lld N=%lld K=%lld)", name,
                 (long long)M, (long long)N, (long long)K);
-    FGB_REQUIRE(M < (1ll << 31) && N < (1ll << 31) && K < (1ll << 23), FGB_EINVAL,
-                "%s: M and N must be below 2^31 and K below 2^23", name);
+    FGB_REQUIRE(M < (1ll << 31) && N < (1ll << 29) && K < (1ll << 23), FGB_EINVAL,
+                "%s: M must be below 2^31, N below 2^29 and K below 2^23", name);
     FGB_REQUIRE(d_dtype == FGB_F32 || d_dtype == FGB_BF16, FGB_EUNSUPPORTED, "%s: d_dtype must be FGB_F32 or FGB_BF16",
                 name);
     return FGB_OK;
@@ -373,7 +375,6 @@ static int launch_mx4(const char *name, const Mx4Args &p, int a_fmt, int d_dtype
     // 16-row blocks, per expert for a grouped product: half a padding to 16 off the
     // average, since M_cap is a bound
     const int64_t rows = p.offs ? p.M / p.G - 8 : p.M, blocks = rows > 16 ? (rows + 15) / 16 : 1;
-    FGB_REQUIRE((p.N / 16 + 8) * 64 < (1ll << 31), FGB_EINVAL, "%s: too many tiles", name);
     if (a_fmt == FGB_E4M3)
         launch_narrow_for<true>(p, blocks, bf16, st);
     else

@@ -610,7 +610,7 @@ int mxfp4_quant(const void *x, int x_dtype, int G, int64_t rows, int64_t cols, i
  *   qt, st  the transposes, [G, cols, R] with R = rows rounded up to 32: codes
  *           [G, cols, R/2], scales [G, ceil(R/256), cols, 8]; columns >= rows hold code 0,
  *           and the last group's scale comes from the rows that exist.
- * rows below 2^23.
+ * rows below 2^23, G below 2^16; cols of an FP32 x below 2^30 - 255.
  */
 int mxfp4_quant_t(const void *x, int x_dtype, int G, int64_t rows, int64_t cols, int64_t ldx, int rule, uint8_t *q,
                   uint8_t *s, uint8_t *qt, uint8_t *st, void *stream);
@@ -630,8 +630,8 @@ int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols
  *   d, d_dtype   : D [M, N], ld ldd, FGB_F32 or FGB_BF16 (round to nearest even);
  *                  FP32 output needs ldd < 2^23 (else FGB_EUNSUPPORTED);
  *                  accumulate != 0 (FP32 only): D += A * B^T.
- * M, N >= 0 (0: nothing is written); K = 0: D = 0 (or unchanged when
- * accumulating).  lda and ldb multiples of 16 below 2^23; a, b and an MXFP4 sa
+ * 0 <= M < 2^31, 0 <= N < 2^29 (0: nothing is written), K < 2^23; K = 0: D = 0 (or
+ * unchanged when accumulating).  lda and ldb multiples of 16 below 2^23; a, b and an MXFP4 sa
  * 16-byte aligned, sb 8-byte (an expert's slice of a stack), an E4M3 A's scales and
  * D at their element's size.  With an
  * E4M3 A each code times its scale becomes a bf16 (exact wherever the value has a

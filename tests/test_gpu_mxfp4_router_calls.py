@@ -88,3 +88,21 @@ def test_slices_of_stacked_scales():
     got = m.mxfp4_grouped_gemm(xq[1], xs[1], q[1:3], s[1:3], off, a_fmt=m.E2M1)
     want = m.mxfp4_grouped_gemm(xq[1].clone(), xs[1].clone(), q[1:3].clone(), s[1:3].clone(), off, a_fmt=m.E2M1)
     assert torch.equal(got, want)
+
+
+def test_more_tiles_than_one_launch_holds():
+    """2^24 workgroups of 256 threads are more than a launch takes: many short matrices, and 2^35 values back."""
+    m = fgb()
+    G = (1 << 24) + 5
+    x = torch.empty((G, 1, 32), dtype=torch.bfloat16, device=DEV).normal_()
+    q, s = m.mxfp4_quant(x)
+    flat, fs = m.mxfp4_quant(x.view(G, 32))  # rows of one matrix: 32 to a workgroup
+    assert torch.equal(q.view(G, 16), flat)
+    assert torch.equal(s.view(G, 8), fs.view(G, 8))
+    del x, q, s, flat, fs
+    rows, cols = (1 << 22) + 3, 8192
+    q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=DEV).random_()
+    s = torch.empty((cols // 256, rows, 8), dtype=torch.uint8, device=DEV).random_(120, 135)
+    d = m.mxfp4_dequant(q, s, out_dtype=torch.bfloat16)
+    for r in (slice(0, 3), slice((1 << 22) - 2, rows)):
+        assert torch.equal(d[r], m.mxfp4_dequant(q[r].contiguous(), s[:, r].contiguous(), out_dtype=torch.bfloat16))

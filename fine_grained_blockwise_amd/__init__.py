@@ -1005,6 +1005,8 @@ def mxfp4_gemm(a, sa, b, sb, a_fmt=E2M1, out_dtype=torch.bfloat16, d=None, accum
     """D = A * B^T with MXFP4 weights b [N, K/2]: A in MXFP4 (a [M, K/2]) or, with a_fmt E4M3, in E4M3 codes
     [M, K] with 1x128 scales -> D [M, N]."""
     name = "mxfp4_gemm"
+    if accumulate and d is None:
+        raise ValueError(f"{name}: accumulate needs d")
     M, K, sa_shape = _mxfp4_a(a, a_fmt, name)
     if b.dim() != 2 or 2 * b.shape[1] != K:
         raise ValueError(f"{name}: b must be [N, K/2] with the same K as a")

@@ -106,3 +106,15 @@ def test_more_tiles_than_one_launch_holds():
     d = m.mxfp4_dequant(q, s, out_dtype=torch.bfloat16)
     for r in (slice(0, 3), slice((1 << 22) - 2, rows)):
         assert torch.equal(d[r], m.mxfp4_dequant(q[r].contiguous(), s[:, r].contiguous(), out_dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_accumulating_needs_a_sum_to_add_to(M):
+    m = fgb()
+    a, sa = m.mxfp4_quant(randn(M, 256))
+    b, sb = m.mxfp4_quant(randn(16, 256, seed=1))
+    with pytest.raises(ValueError, match="accumulate needs d"):
+        m.mxfp4_gemm(a, sa, b, sb, out_dtype=torch.float32, accumulate=True)
+    d = torch.ones((M, 16), device=DEV)
+    m.mxfp4_gemm(a, sa, b, sb, d=d, accumulate=True)
+    assert torch.equal(d, 1 + m.mxfp4_gemm(a, sa, b, sb, out_dtype=torch.float32))

@@ -17,6 +17,10 @@ namespace fgb {
 int set_error(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 void clear_error();
 
+// Workgroups (of up to 256 threads) of one launch: the runtime keeps the low 32 bits of a
+// launch's threads, without an error, so larger work goes in several launches.
+constexpr int64_t LAUNCH_BLOCKS = 1 << 23;
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ---------------------------------------------------------------------------

@@ -25,10 +25,10 @@ __global__ __launch_bounds__(256) void mx2_quant_kernel(const uint16_t *__restri
                                                         int64_t C, int64_t g1, int64_t ng,
                                                         uint8_t *__restrict__ q,
                                                         uint8_t *__restrict__ s2,
-                                                        float *__restrict__ s1)
+                                                        float *__restrict__ s1, int64_t first)
 {
     __shared__ uint32_t red[4];
-    const int64_t r = blockIdx.x / ng, g = blockIdx.x % ng;
+    const int64_t r = (first + blockIdx.x) / ng, g = (first + blockIdx.x) % ng;
     const int64_t c0 = g * g1;
     const int64_t len = min(g1, C - c0);
     const int64_t nch = len / 8;
@@ -148,13 +148,16 @@ extern "C" int mx2_quant_rule(const void *x, int64_t R, int64_t C, int64_t g1, i
         return FGB_OK;
     int64_t ng = (C + g1 - 1) / g1;
     FGB_REQUIRE(R * ng < (1ll << 31), FGB_EINVAL, "mx2_quant: too many groups");
-    if (rule == FGB_SCALE_OCP_FLOOR)
-        mx2_quant_kernel<RULE_OCP_FLOOR><<<(unsigned)(R * ng), 256, 0, (hipStream_t)stream>>>((const uint16_t *)x, R, C, g1,
-                                                                                              ng, q, s2, s1);
-    else
-        mx2_quant_kernel<RULE_CEIL><<<(unsigned)(R * ng), 256, 0, (hipStream_t)stream>>>((const uint16_t *)x, R, C, g1, ng,
-                                                                                         q, s2, s1);
-    FGB_LAUNCHED("mx2_quant");
+    for (int64_t first = 0; first < R * ng; first += LAUNCH_BLOCKS) {
+        const unsigned grid = (unsigned)(R * ng - first < LAUNCH_BLOCKS ? R * ng - first : LAUNCH_BLOCKS);
+        if (rule == FGB_SCALE_OCP_FLOOR)
+            mx2_quant_kernel<RULE_OCP_FLOOR><<<grid, 256, 0, (hipStream_t)stream>>>((const uint16_t *)x, R, C, g1, ng, q,
+                                                                                    s2, s1, first);
+        else
+            mx2_quant_kernel<RULE_CEIL><<<grid, 256, 0, (hipStream_t)stream>>>((const uint16_t *)x, R, C, g1, ng, q, s2,
+                                                                               s1, first);
+        FGB_LAUNCHED("mx2_quant");
+    }
     return FGB_OK;
 }
 

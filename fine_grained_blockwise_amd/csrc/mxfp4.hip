@@ -398,10 +398,6 @@ __global__ __launch_bounds__(256) void mxfp4_dequant_kernel(const uint8_t *q, co
     }
 }
 
-// Workgroups of one launch: the runtime keeps the low 32 bits of a launch's threads, without
-// an error, so larger work goes in several launches (256 threads each: 2^31 threads).
-constexpr int64_t LAUNCH_BLOCKS = 1 << 23;
-
 static int check_quant(const char *name, const void *x, int x_dtype, int G, int64_t rows, int64_t cols, int64_t ldx, int rule,
                        const void *q, const void *s)
 {

@@ -118,3 +118,11 @@ def test_accumulating_needs_a_sum_to_add_to(M):
     d = torch.ones((M, 16), device=DEV)
     m.mxfp4_gemm(a, sa, b, sb, d=d, accumulate=True)
     assert torch.equal(d, 1 + m.mxfp4_gemm(a, sa, b, sb, out_dtype=torch.float32))
+
+
+def test_more_moss_groups_than_one_launch_holds():
+    m = fgb()
+    x = torch.empty(((1 << 16) + 1, 8192), dtype=torch.bfloat16, device=DEV).normal_()
+    q, s2, s1 = m.mx2_quant(x, g1=32)  # 256 groups a row
+    for r in (slice(0, 2), slice((1 << 15) - 1, (1 << 15) + 1), slice((1 << 16) - 1, (1 << 16) + 1)):
+        assert equal((q[r], s2[r], s1[r]), m.mx2_quant(x[r].contiguous(), g1=32))

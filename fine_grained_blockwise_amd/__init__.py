@@ -24,7 +24,7 @@ __all__ = [
     "fp8_direct_transpose_fmt", "mx2_quant_rule", "fp8_block_gemm_fmt", "fp8_grouped_gemm_masked",
     "permute_pad_noalloc", "PERMUTE_PAD_NOALLOC_SCRATCH_BYTES", "fgb_hbm_probe",
     "PROBE_COPY", "PROBE_READ", "PROBE_FILL", "PROBE_STRIDED_READ", "PROBE_STRIDED_WRITE",
-    "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm", "mxfp4_grouped_gemm",
+    "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm", "mxfp4_grouped_gemm", "mxfp4_gemm_tiled",
     "moe_router", "moe_router_backward", "moe_router_workspace_size", "ROUTER_SOFTMAX", "ROUTER_SIGMOID",
     "E4M3", "E5M2", "E2M1", "SCALE_CEIL", "SCALE_OCP_FLOOR", "F32", "BF16", "ROW1x128", "ROW1x32", "BLOCK128", "GEMM_EXACT", "GEMM_FAST",
 ]
@@ -50,7 +50,7 @@ SYMBOLS = [
     "fp8_quant_rowwise_fmt", "fp8_dequant_fmt", "fgb_fp8_encode", "fp8_direct_transpose_fmt", "mx2_quant_rule",
     "fp8_block_gemm_fmt", "fp8_grouped_gemm_masked", "fp8_quant_blockwise_t", "swiglu_f32", "dswiglu_f32",
     "permute_pad_noalloc", "fgb_hbm_probe", "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm",
-    "mxfp4_grouped_gemm", "moe_router", "moe_router_workspace_size", "moe_router_backward",
+    "mxfp4_grouped_gemm", "mxfp4_gemm_tiled", "moe_router", "moe_router_workspace_size", "moe_router_backward",
 ]
 
 
@@ -113,6 +113,7 @@ _SIG = {
     "mxfp4_dequant": (_i32, [_p, _p, _i64, _i64, _p, _i32, _p]),
     "mxfp4_gemm": (_i32, [_p, _p, _i32, _p, _p, _i64, _i64, _i64, _i64, _i64, _p, _i32, _i64, _i32, _p]),
     "mxfp4_grouped_gemm": (_i32, [_p, _p, _i32, _p, _p, _p, _i32, _i64, _i64, _i64, _p, _i32, _p]),
+    "mxfp4_gemm_tiled": (_i32, [_i32, _i64, _i64, _i64, _i32]),
     "moe_router": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _i32, _i32, _f32, _f32, _p, _p, _p, _p, _p, _sz, _p]),
     "moe_router_workspace_size": (_sz, [_i64, _i32]),
     "moe_router_backward": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _p, _p, _p, _i32, _i32, _f32, _f32, _p, _i64,
@@ -1048,6 +1049,12 @@ def mxfp4_grouped_gemm(a, sa, b, sb, group_offsets, a_fmt=E4M3, out_dtype=torch.
     _call(name, a.data_ptr(), sa.data_ptr(), a_fmt, b.data_ptr(), sb.data_ptr(), group_offsets.data_ptr(), G, M_cap, N,
           K, d.data_ptr(), _dtype_code(d), _stream(a))
     return d
+
+
+def mxfp4_gemm_tiled(M, N, K, a_fmt=E2M1, groups=0):
+    """Whether a product of these sizes runs on 256 x 256 tiles or on the kernel for few rows; groups: the experts of
+    mxfp4_grouped_gemm (M is then its rows' bound), 0 for mxfp4_gemm."""
+    return bool(_lib.mxfp4_gemm_tiled(a_fmt, M, N, K, groups))
 
 
 def moe_router_workspace_size(T, E):

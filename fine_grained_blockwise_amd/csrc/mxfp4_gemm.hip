@@ -354,23 +354,24 @@ template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16
 // 128x28672x8192 63 / 53, 32 experts of 32 rows (4096x7168) 114 / 131; E4M3 A:
 // 1024x2048x7168 53 / 115, 256x7168x2048 21 / 38, 768x7168x2048 59 / 39, 128x28672x8192
 // 112 / 133, 192x28672x8192 163 / 134, 32 experts of 64 rows 221 / 331, of 128 417 / 339.
-static bool takes_narrow(const Mx4Args &p, int a_fmt)
+// G: experts, 0 for a dense product.
+static bool takes_narrow(int64_t M, int64_t N, int64_t K, int G, int a_fmt)
 {
-    const bool a8 = a_fmt == FGB_E4M3;
-    const double step_us = a8 ? (double)(p.K / 128) * 1.9 : (double)((p.K + 255) / 256) * 1.25;
-    const double tile_us = (8.0 + step_us) * (p.offs ? 1.4 : 1.0);
-    const int64_t tiles = ((p.M + 255) / 256 + (p.offs ? p.G / 2 : 0)) * ((p.N + 255) / 256);
-    double work = (double)p.M * (double)p.N;
-    if (!p.offs && p.M > 64)
-        work = (double)(((p.M + 63) / 64 * ((p.N + 127) / 128) + 255) / 256 * 256) * (64 * 128);
-    const double narrow_us = 2e-9 * work * (double)p.K / (a8 ? 0.55 : 0.78);
+    const bool a8 = a_fmt == FGB_E4M3, grouped = G > 0;
+    const double step_us = a8 ? (double)(K / 128) * 1.9 : (double)((K + 255) / 256) * 1.25;
+    const double tile_us = (8.0 + step_us) * (grouped ? 1.4 : 1.0);
+    const int64_t tiles = ((M + 255) / 256 + G / 2) * ((N + 255) / 256);
+    double work = (double)M * (double)N;
+    if (!grouped && M > 64)
+        work = (double)(((M + 63) / 64 * ((N + 127) / 128) + 255) / 256 * 256) * (64 * 128);
+    const double narrow_us = 2e-9 * work * (double)K / (a8 ? 0.55 : 0.78);
     return narrow_us <= tile_us * (double)((tiles + 255) / 256);
 }
 
 static int launch_mx4(const char *name, const Mx4Args &p, int a_fmt, int d_dtype, hipStream_t st)
 {
     const bool bf16 = d_dtype == FGB_BF16;
-    if (!takes_narrow(p, a_fmt))
+    if (!takes_narrow(p.M, p.N, p.K, p.offs ? p.G : 0, a_fmt))
         return p.offs ? launch_tiled<GK_M>(p, a_fmt, bf16, st) : launch_tiled<GK_NONE>(p, a_fmt, bf16, st);
     // 16-row blocks, per expert for a grouped product: half a padding to 16 off the
     // average, since M_cap is a bound
@@ -386,6 +387,14 @@ static int launch_mx4(const char *name, const Mx4Args &p, int a_fmt, int d_dtype
 } // namespace fgb
 
 using namespace fgb;
+
+extern "C" int mxfp4_gemm_tiled(int a_fmt, int64_t M, int64_t N, int64_t K, int G)
+{
+    clear_error();
+    if (check_mx4("mxfp4_gemm_tiled", a_fmt, M, N, K, FGB_BF16) != FGB_OK || G < 0)
+        return 0;
+    return M > 0 && N > 0 && !takes_narrow(M, N, K, G, a_fmt);
+}
 
 extern "C" int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b, const uint8_t *sb, int64_t M,
                           int64_t N, int64_t K, int64_t lda, int64_t ldb, void *d, int d_dtype, int64_t ldd,

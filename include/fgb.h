@@ -636,8 +636,9 @@ int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols
  * D at their element's size.  With an
  * E4M3 A each code times its scale becomes a bf16 (exact wherever the value has a
  * bf16 representation) and products are exact; with an MXFP4 A the matrix unit
- * takes codes and scales, its sums measured at FP32 rounding.  Results do not
- * depend on M: a row comes out the same in any batch that takes the same kernel.
+ * takes codes and scales, its sums measured at FP32 rounding.  Calls of the same
+ * sizes give the same bits; the order of a row's sums, and with it their low bits,
+ * depends on the sizes (M among them; for experts M_cap / G).
  */
 int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b, const uint8_t *sb, int64_t M, int64_t N,
                int64_t K, int64_t lda, int64_t ldb, void *d, int d_dtype, int64_t ldd, int accumulate, void *stream);
@@ -656,6 +657,13 @@ int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b,
 int mxfp4_grouped_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b, const uint8_t *sb,
                        const int32_t *group_offsets, int G, int64_t M_cap, int64_t N, int64_t K, void *d, int d_dtype,
                        void *stream);
+
+/*
+ * mxfp4_gemm_tiled -- 1 if a product of these sizes runs on 256 x 256 tiles, 0 if on
+ * the kernel for few rows, which splits K.  G: the experts of mxfp4_grouped_gemm (M is
+ * then M_cap), 0 for mxfp4_gemm.  Both hold the same bounds.
+ */
+int mxfp4_gemm_tiled(int a_fmt, int64_t M, int64_t N, int64_t K, int G);
 
 /*
  * moe_router -- the experts of each token, their weights, the slots per expert

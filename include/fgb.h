@@ -682,6 +682,7 @@ int mxfp4_gemm_tiled(int a_fmt, int64_t M, int64_t N, int64_t K, int G);
  *   counts[e]   = slots that chose e, counts[E] = the live tokens n
  *   loss        = loss_coef * E / (topk n^2) * sum_e counts[e] sum_t p[t][e] (0 if n = 0);
  *                 NULL: not computed
+ *   A row of nothing but -inf and NaN is not live, so NaN goes unseen there.
  *   A NaN logit of a live token (with softmax scores +inf too) makes NaN of what sums
  *   over it: the loss, softmax and renormed weights, and the token's gradient.
  *   workspace: moe_router_workspace_size(T, E) bytes (0 for a few tokens, then it may

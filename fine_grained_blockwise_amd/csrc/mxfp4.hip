@@ -130,7 +130,8 @@ __device__ __forceinline__ uint32_t four_bytes(uint32_t b)
 
 // Rows: a workgroup takes 32 rows x 256 columns (one scale step), a half-wave a row
 // and four rows in flight, so that the step's scales leave as whole lines.  HBM-bound:
-// 2 (4) bytes read and 17/32 written per element.  8192x28672 bf16: 103 us, 5.8 TB/s.
+// 2 (4) bytes read and 17/32 written per element.  8192x28672 bf16: 103 us, 5.8 TB/s;
+// fp32: 192 us, 5.5 TB/s.
 template <bool BF16, int RULE>
 __global__ __launch_bounds__(256) void mxfp4_quant_kernel(const void *x, int64_t rows, int64_t cols, int64_t ldx,
                                                           uint8_t *q, uint8_t *s, int steps, int tiles_m, int first)
@@ -277,7 +278,7 @@ __global__ __launch_bounds__(512) void mxfp4_quant_t_bf16_kernel(const void *x, 
     }
 }
 
-// The same for fp32: a workgroup takes 128 rows x 128 columns,
+// The same for fp32 (8192x7168: 63 us, 4.7 TB/s): a workgroup takes 128 rows x 128 columns,
 // quantises the rows as it reads them, keeps the values in LDS and quantises the
 // columns from there.  Row r of the tile starts at word r * 128 + (r / 32) * 16,
 // so the four 32-row groups of a column, read by neighbouring lanes, sit 16 banks

@@ -3,9 +3,9 @@
 // B holds E2M1 codes with 1x32 scales; A the same, or E4M3 codes with 1x128 scales.
 //   E2M1 A: the scaled matrix instruction takes 32 codes and one scale byte per
 //     lane.  A product of two E2M1 values is a multiple of 1/4 up to 36, so the 32
-//     products of a group add up exactly, and the unit's sums across groups were
-//     measured at FP32 rounding (worst 5.6e-7 of the largest product with scales
-//     2^-20 .. 2^20 apart; scale byte 255 gives NaN).
+//     products of a group add up exactly; with the unit's sums across groups, scales
+//     2^-20 .. 2^20 apart among them, D stays within the bound of K products summed in
+//     FP32 (the tests hold it there).  Scale byte 255 gives NaN.
 //   E4M3 A: both operands become bf16 with their power of two folded in (exact),
 //     multiplied on the bf16 matrix unit with FP32 sums, as FGB_GEMM_EXACT does.
 #include "gemm_kernel.h"
@@ -277,9 +277,11 @@ template <bool A8, int MB, int NB, int W> static void launch_narrow(const Mx4Arg
 }
 
 // The narrow kernel's tile: the largest of (16 MB rows, 16 NB columns) whose rows are
-// needed and whose workgroups still reach three quarters of the 256 CUs.  For one row
+// needed and whose tiles still number three quarters of the 256 CUs.  (Tiles, not
+// workgroups that run at once: a column tile's chunks stay on one XCD, so fewer than
+// eight column tiles leave XCDs idle, which this count does not see.)  For one row
 // of 2048x7168, 28672x8192: (1, 1) 5.7, 32 us, (1, 4) 12, 29 us; 64 rows: (1, 2) 8.7,
-// 91 us, (4, 4) 20, 44 us, (4, 8) -, 38 us (E4M3 A 76 and 64 us: fewer reads of A, one
+// 91 us, (4, 4) 20, 45 us, (4, 8) -, 38 us (E4M3 A 74 and 53 us: fewer reads of A, one
 // wave a SIMD).
 template <bool A8> static void launch_narrow_for(const Mx4Args &p, int64_t blocks, bool bf16, hipStream_t st)
 {
@@ -347,13 +349,15 @@ template <int GK> static int launch_tiled(const Mx4Args &x, int a_fmt, bool bf16
 // tiles 256 at a time, each round 8 us and 1.25 us a 256-element step (1.9 us a
 // 128-element step with an E4M3 A), 1.4 times that where every tile reads other
 // weights (experts of few rows); the narrow one reads the weights once per 16-64 rows
-// and reaches 0.78 (0.55) PFLOP/s, less only where it is bound by bytes and far ahead;
-// its 64 x 128 blocks of a dense product of more than 64 rows run 256 at a time too.
+// and reaches 0.78 (0.55 at K = 2048, 0.7 at K = 7168) PFLOP/s, less only where it is
+// bound by bytes and far ahead; its 64 x 128 blocks of a dense product of more than 64
+// rows run 256 at a time too.
 // Measured, narrow against tiled, MXFP4 A: 512x2048x7168 19 / 42 us, 1024x2048x7168
-// 28 / 42, 256x7168x2048 14.5 / 18, 320x7168x2048 26 / 18.6, 64x28672x8192 40 / 56,
-// 128x28672x8192 63 / 53, 32 experts of 32 rows (4096x7168) 114 / 131; E4M3 A:
-// 1024x2048x7168 53 / 115, 256x7168x2048 21 / 38, 768x7168x2048 59 / 39, 128x28672x8192
-// 112 / 133, 192x28672x8192 163 / 134, 32 experts of 64 rows 221 / 331, of 128 417 / 339.
+// 29 / 42, 256x7168x2048 15 / 18, 320x7168x2048 27 / 18.6, 64x28672x8192 38 / 53,
+// 128x28672x8192 64 / 52, 32 experts of 32 rows (4096x7168) 113 / 135; E4M3 A:
+// 1024x2048x7168 42 / 115, 256x7168x2048 21 / 38, 768x7168x2048 58 / 40, 128x28672x8192
+// 98 / 134, 192x28672x8192 145 / 134, 32 experts of 64 rows 178 / 332, of 128 327 / 332
+// (7168x2048: 260 / 199).
 // G: experts, 0 for a dense product.
 static bool takes_narrow(int64_t M, int64_t N, int64_t K, int G, int a_fmt)
 {

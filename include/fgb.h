@@ -631,14 +631,14 @@ int mxfp4_dequant(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols
  *                  FP32 output needs ldd < 2^23 (else FGB_EUNSUPPORTED);
  *                  accumulate != 0 (FP32 only): D += A * B^T.
  * 0 <= M < 2^31, 0 <= N < 2^29 (0: nothing is written), K < 2^23; K = 0: D = 0 (or
- * unchanged when accumulating).  lda and ldb multiples of 16 below 2^23; a, b and an MXFP4 sa
- * 16-byte aligned, sb 8-byte (an expert's slice of a stack), an E4M3 A's scales and
- * D at their element's size.  With an
- * E4M3 A each code times its scale becomes a bf16 (exact wherever the value has a
- * bf16 representation) and products are exact; with an MXFP4 A the matrix unit
- * takes codes and scales, its sums measured at FP32 rounding.  Calls of the same
- * sizes give the same bits; the order of a row's sums, and with it their low bits,
- * depends on the sizes (M among them; for experts M_cap / G).
+ * unchanged when accumulating).  lda and ldb multiples of 16 below 2^23; a, b and an
+ * MXFP4 sa 16-byte aligned, sb 8-byte (an expert's slice of a stack), an E4M3 A's
+ * scales and D at their element's size.  With an E4M3 A each code times its scale
+ * becomes a bf16 (exact wherever the value has a bf16 representation) and products
+ * are exact; with an MXFP4 A the matrix unit takes codes and scales, and D stays
+ * within the bound of K products summed in FP32, K 2^-24 sum |a b|.  Calls of the
+ * same sizes give the same bits; the order of a row's sums, and with it their low
+ * bits, depends on the sizes (M among them; for experts M_cap / G).
  */
 int mxfp4_gemm(const uint8_t *a, const uint8_t *sa, int a_fmt, const uint8_t *b, const uint8_t *sb, int64_t M, int64_t N,
                int64_t K, int64_t lda, int64_t ldb, void *d, int d_dtype, int64_t ldd, int accumulate, void *stream);

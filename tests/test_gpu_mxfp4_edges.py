@@ -56,3 +56,16 @@ def test_every_quantizer_at_the_edges(dtype, rule):
     cols = torch.zeros((32, (n + 31) // 32 * 32), dtype=dtype)
     cols[:, :n] = t.t()
     same(*m.mxfp4_quant_t(cols.to(DEV), rule=rule)[2:], q, s, n)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("G,rows,cols", [(3, 45, 96), (5, 300, 288), (40, 257, 1056)])
+def test_stacks_are_their_matrices(G, rows, cols, dtype):
+    import fine_grained_blockwise_amd as m
+    x = torch.randn((G, rows, cols), generator=torch.Generator().manual_seed(G)).to(dtype).to(DEV)
+    alone = [m.mxfp4_quant_t(x[g]) for g in range(G)]
+    for got in (m.mxfp4_quant(x), m.mxfp4_quant_t(x)):
+        for i, t in enumerate(got):
+            assert all(torch.equal(t[g], alone[g][i]) for g in range(G))
+    wq, ws = O.quant(x[G - 1].double().cpu().numpy())
+    assert np.array_equal(alone[-1][0].cpu().numpy(), wq) and np.array_equal(alone[-1][1].cpu().numpy(), ws)

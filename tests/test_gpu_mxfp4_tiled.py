@@ -171,3 +171,24 @@ def test_linear_training_step():
     check(m.mxfp4_gemm(gq, gs, wqt, wst), val(gq, gs), val(wqt, wst))
     dw = m.mxfp4_gemm(gqt, gst, xqt, xst, out_dtype=torch.float32)
     check(dw, val(gqt, gst), val(xqt, xst))
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [("e2m1", 2049, 2309, 1120), ("e4m3", 2305, 2817, 1280)])
+def test_in_a_graph(fmt, M, N, K):
+    """Captured once, replayed on other activations with eager work between: the eager result's bits."""
+    tiled(M, N, K, fmt)
+    m = fgb()
+    a, sa, _ = operand_a(fmt, M, K, 1)
+    b, sb, _ = e2m1(N, K, 2)
+    m.mxfp4_gemm(a, sa, b, sb, a_fmt=code(fmt))  # once eagerly before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = m.mxfp4_gemm(a, sa, b, sb, a_fmt=code(fmt))
+    for seed in (1, 3, 4):
+        for t, new in zip((a, sa), operand_a(fmt, M, K, seed)):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        got, want = held.clone(), m.mxfp4_gemm(a, sa, b, sb, a_fmt=code(fmt))
+        assert torch.equal(got, want)

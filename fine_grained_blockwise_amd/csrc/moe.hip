@@ -199,12 +199,12 @@ __global__ __launch_bounds__(256) void pp_copy_kernel(const uint8_t *__restrict_
                                                       const int32_t *__restrict__ offs,
                                                       uint8_t *__restrict__ out_q,
                                                       uint8_t *__restrict__ out_s, int64_t tok_blocks,
-                                                      int64_t M_cap)
+                                                      int64_t M_cap, int64_t first)
 {
     const int lane = lane_id(), wave = threadIdx.x >> 6;
-    const int64_t H16 = H / 16, H128 = H / 128;
-    if ((int64_t)blockIdx.x < tok_blocks) {
-        int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    const int64_t H16 = H / 16, H128 = H / 128, block = first + blockIdx.x;
+    if (block < tok_blocks) {
+        int64_t t = block * 4 + wave;
         if (t >= T)
             return;
         int32_t my_row = lane < topk ? row_map[t * topk + lane] : -1;
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256) void pp_copy_kernel(const uint8_t *__restrict_
             }
         }
     } else {
-        int64_t pidx = ((int64_t)blockIdx.x - tok_blocks) * 4 + wave;
+        int64_t pidx = (block - tok_blocks) * 4 + wave;
         if (pad <= 1 || pidx >= (int64_t)(pad - 1) * G)
             return;
         int e = (int)(pidx / (pad - 1)), j = (int)(pidx % (pad - 1));
@@ -825,9 +825,10 @@ static int permute_pad_launch(const uint8_t *xq, const uint8_t *xs, const int32_
     int64_t tok_blocks = (T + 3) / 4;
     int64_t pad_blocks = ((int64_t)(pad_multiple - 1) * G + 3) / 4;
     int64_t grid = tok_blocks + pad_blocks;
-    if (grid > 0) {
-        pp_copy_kernel<<<(unsigned)grid, 256, 0, st>>>(xq, xs, row_map, T, topk, G, H, pad_multiple,
-                                                      w.total, group_offsets, out_q, out_s, tok_blocks, M_cap);
+    for (int64_t first = 0; first < grid; first += LAUNCH_BLOCKS) {
+        const unsigned n = (unsigned)(grid - first < LAUNCH_BLOCKS ? grid - first : LAUNCH_BLOCKS);
+        pp_copy_kernel<<<n, 256, 0, st>>>(xq, xs, row_map, T, topk, G, H, pad_multiple, w.total, group_offsets, out_q,
+                                          out_s, tok_blocks, M_cap, first);
         FGB_LAUNCHED("permute_pad/copy");
     }
     return FGB_OK;

@@ -126,3 +126,19 @@ def test_more_moss_groups_than_one_launch_holds():
     q, s2, s1 = m.mx2_quant(x, g1=32)  # 256 groups a row
     for r in (slice(0, 2), slice((1 << 15) - 1, (1 << 15) + 1), slice((1 << 16) - 1, (1 << 16) + 1)):
         assert equal((q[r], s2[r], s1[r]), m.mx2_quant(x[r].contiguous(), g1=32))
+
+
+def test_more_tokens_than_one_launch_permutes():
+    m = fgb()
+    T, G, H = (1 << 26) + 5, 4, 128
+    xq = torch.empty((T, H), dtype=torch.uint8, device=DEV).random_()
+    xs = torch.empty((T, 1), dtype=torch.uint8, device=DEV).random_()
+    idx = torch.empty((T, 1), dtype=torch.int32, device=DEV).random_(0, G)
+    q, s, row_map, offs = m.permute_pad(xq, xs, idx, G)
+    at = row_map[:, 0].long()
+    for lo in range(0, T, 1 << 24):
+        part = slice(lo, lo + (1 << 24))
+        assert torch.equal(q[at[part]], xq[part]) and torch.equal(s[at[part]], xs[part])
+    counts, off = torch.bincount(idx[:, 0], minlength=G).tolist(), offs.tolist()
+    for g in range(G):
+        assert bool((q[off[g] + counts[g]:off[g + 1]] == 0).all())

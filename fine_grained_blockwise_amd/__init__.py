@@ -26,6 +26,8 @@ __all__ = [
     "PROBE_COPY", "PROBE_READ", "PROBE_FILL", "PROBE_STRIDED_READ", "PROBE_STRIDED_WRITE",
     "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm", "mxfp4_grouped_gemm", "mxfp4_gemm_tiled",
     "moe_router", "moe_router_backward", "moe_router_workspace_size", "ROUTER_SOFTMAX", "ROUTER_SIGMOID",
+    "moe_bias_update", "rmsnorm_quant", "rmsnorm_backward", "rmsnorm_backward_workspace_size",
+    "grad_sumsq", "grad_clip", "grad_sumsq_workspace_size",
     "E4M3", "E5M2", "E2M1", "SCALE_CEIL", "SCALE_OCP_FLOOR", "F32", "BF16", "ROW1x128", "ROW1x32", "BLOCK128", "GEMM_EXACT", "GEMM_FAST",
 ]
 
@@ -51,6 +53,8 @@ SYMBOLS = [
     "fp8_block_gemm_fmt", "fp8_grouped_gemm_masked", "fp8_quant_blockwise_t", "swiglu_f32", "dswiglu_f32",
     "permute_pad_noalloc", "fgb_hbm_probe", "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm",
     "mxfp4_grouped_gemm", "mxfp4_gemm_tiled", "moe_router", "moe_router_workspace_size", "moe_router_backward",
+    "moe_router_grouped", "moe_bias_update", "rmsnorm_quant", "rmsnorm_backward", "rmsnorm_backward_workspace_size",
+    "grad_sumsq", "grad_sumsq_workspace_size", "grad_clip",
 ]
 
 
@@ -65,7 +69,7 @@ if not os.path.exists(LIB_PATH):
                       "`python -c 'import __graft_entry__ as g; g.build()'`")
 
 _lib = C.CDLL(LIB_PATH)
-_p, _i64, _i32, _sz, _f32 = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float
+_p, _i64, _i32, _sz, _f32, _f64 = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float, C.c_double
 _SIG = {
     "fgb_last_error": (C.c_char_p, []),
     "fgb_version": (C.c_char_p, []),
@@ -118,6 +122,17 @@ _SIG = {
     "moe_router_workspace_size": (_sz, [_i64, _i32]),
     "moe_router_backward": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _p, _p, _p, _i32, _i32, _f32, _f32, _p, _i64,
                                    _p]),
+    "moe_router_grouped": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _f32, _f32, _p, _p,
+                                  _p, _p, _p, _sz, _p]),
+    "moe_bias_update": (_i32, [_p, _p, _i32, _f32, _p, _p]),
+    "rmsnorm_quant": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _p, _i32, _f32, _i32, _p, _i64, _p, _p, _p, _p,
+                             _i32, _i64, _p]),
+    "rmsnorm_backward": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _p, _i32, _p, _p, _i64, _p, _i64, _p, _p,
+                                _sz, _p]),
+    "rmsnorm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "grad_sumsq": (_i32, [_p, _p, _p, _i32, _p, _i32, _p, _sz, _p]),
+    "grad_sumsq_workspace_size": (_sz, [_p, _i32]),
+    "grad_clip": (_i32, [_p, _p, _p, _p, _p, _i32, _f64, _f64, _p, _p, _p, _sz, _p]),
 }
 for _name, (_res, _args) in _SIG.items():
     _f = getattr(_lib, _name)
@@ -138,6 +153,16 @@ def _call(name, *args):
     rc = getattr(_lib, name)(*args)
     if rc != 0:
         raise FgbError(name, rc, _lib.fgb_last_error().decode())
+
+
+def _call_on(dev, name, *args):
+    """_call with `dev` as the current device: a launch goes to the current one, and the stream's handle does not
+    tell (every device's default stream is 0)."""
+    if dev.index == torch.cuda.current_device():
+        _call(name, *args)
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args)
 
 
 def _ptr(t):
@@ -1071,12 +1096,16 @@ def _router_logits(logits, topk, name):
 
 
 def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss_coef=0.0, token_mask=None,
-               workspace=None):
+               workspace=None, bias=None, groups=1, topk_groups=1):
     """Top-k routing of logits [T, E] (fp32/bf16): -> (topk_idx int32 [T, topk], weights fp32 [T, topk],
     counts int32 [E+1], loss fp32 scalar, or None with loss_coef 0).
 
     counts[e] is the number of slots that chose expert e, counts[E] the number of live tokens; token_mask
-    (bool or uint8 [T]) marks padding tokens with 0.  Slots without an expert hold id -1 and weight 0."""
+    (bool or uint8 [T]) marks padding tokens with 0.  Slots without an expert hold id -1 and weight 0.
+
+    bias fp32 [E]: experts are chosen by score + bias (the weights stay the scores').  groups > 1: experts are chosen
+    from the topk_groups best of `groups` runs of E / groups experts, a run's value being the sum of its two largest
+    score + bias, or without a bias its largest logit."""
     name = "moe_router"
     T, E, dt = _router_logits(logits, topk, name)
     if token_mask is not None:
@@ -1085,7 +1114,13 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
         _need(token_mask, f"{name}: token_mask", shape=(T,), contiguous=True)
     if workspace is not None:
         _need(workspace, f"{name}: workspace", dtype=torch.uint8, contiguous=True)
-    dev = _check_dev(logits, token_mask, workspace)
+    if bias is not None:
+        _need(bias, f"{name}: bias", shape=(E,), dtype=torch.float32, contiguous=True)
+    if not 1 <= groups <= 64 or E % groups:
+        raise ValueError(f"{name}: groups must be in [1, 64] and divide E ({E}), got {groups}")
+    if not 1 <= topk_groups <= groups or topk > topk_groups * (E // groups):
+        raise ValueError(f"{name}: topk_groups must be in [1, groups] and hold topk experts, got {topk_groups}")
+    dev = _check_dev(logits, token_mask, workspace, bias)
     if workspace is None:
         need = _lib.moe_router_workspace_size(T, E)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
@@ -1093,9 +1128,13 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
     weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
     counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
     loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef else None
-    _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), score, int(bool(renorm)), scale,
-          loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss), _ptr(workspace),
-          0 if workspace is None else workspace.numel(), _stream(logits))
+    out = (score, int(bool(renorm)), scale, loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss),
+           _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(logits))
+    if bias is None and groups == 1:
+        _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), *out)
+    else:
+        _call_on(dev, "moe_router_grouped", _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), _ptr(bias),
+                 groups, topk_groups, *out)
     return idx, weights, counts, loss
 
 
@@ -1121,3 +1160,231 @@ def moe_router_backward(logits, topk_idx, counts, dweights=None, dloss=None, sco
     _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(topk_idx), _ptr(counts), _ptr(dweights),
           _ptr(dloss), score, int(bool(renorm)), scale, loss_coef, _ptr(dz), E, _stream(logits))
     return dz
+
+
+def moe_bias_update(bias, counts, rate, out=None):
+    """The router's bias for the next step: bias[e] + rate where fewer slots than the mean chose expert e, - rate where
+    more did.  bias fp32 [E], counts int32 [E+1] as moe_router gives them -> out fp32 [E] (it may be bias)."""
+    name = "moe_bias_update"
+    if bias.dim() != 1:
+        raise ValueError(f"{name}: bias must be [E]")
+    E = bias.shape[0]
+    _need(bias, f"{name}: bias", dtype=torch.float32, contiguous=True)
+    _need(counts, f"{name}: counts", shape=(E + 1,), dtype=torch.int32, contiguous=True)
+    if out is not None:
+        _need(out, f"{name}: out", shape=(E,), dtype=torch.float32, contiguous=True)
+    dev = _check_dev(bias, counts, out)
+    if out is None:
+        out = torch.empty_like(bias)
+    _call_on(dev, name, bias.data_ptr(), counts.data_ptr(), E, rate, out.data_ptr(), _stream(bias))
+    return out
+
+
+# ---------------------------------------------------------------------------
+def _norm_rows(t, name, shape=None):
+    """t and its row stride, copied where rows are not 16-byte aligned runs."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be 2-D" if shape is None else f"{name} must have shape {tuple(shape)}, got "
+                         f"{tuple(t.shape)}")
+    _dtype_code(t)
+    if not t.is_cuda:
+        raise ValueError("all tensors must be on the GPU")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols or ld * t.element_size() % 16 or t.data_ptr() % 16:
+        return t.clone(memory_format=torch.contiguous_format), cols
+    return t, ld
+
+
+def _norm_out(t, name, shape, dtype):
+    """A given output of the norm: it is written in place, so its layout has to fit; its row stride."""
+    _need(t, name, shape=shape, dtype=dtype)
+    rows, cols = shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols or ld * t.element_size() % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have 16-byte aligned rows of unit stride")
+    return ld
+
+
+def _norm_weight(weight, cols, name):
+    _need(weight, f"{name}: weight", shape=(cols,))
+    _dtype_code(weight)
+    if not weight.is_contiguous() or weight.data_ptr() % 16:
+        weight = weight.clone(memory_format=torch.contiguous_format)
+    return weight
+
+
+def _norm_cols(cols, name):
+    if cols % 32 or not 0 < cols <= 32768:
+        raise ValueError(f"{name}: cols must be a multiple of 32 up to 32768, got {cols}")
+
+
+def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_dtype=None, h=None):
+    """RMSNorm of x + residual into E4M3 codes: -> (q uint8 [rows, cols], s uint8 [rows, cols/group], y, h,
+    rstd fp32 [rows]).
+
+    h is the sum in the residual's type (x itself without a residual), y = h * rstd * weight in y_dtype (None: not
+    written), q and s the codes and scales of y before its rounding (None with quant=False).  h= takes a tensor for
+    the sum; it may be the residual itself."""
+    name = "rmsnorm_quant"
+    if group not in (32, 128):
+        raise ValueError(f"{name}: group must be 32 or 128, got {group}")
+    if not quant and y_dtype is None:
+        raise ValueError(f"{name}: y_dtype is required with quant=False")
+    if not eps > 0:
+        raise ValueError(f"{name}: eps must be positive")
+    if h is not None and residual is None:
+        raise ValueError(f"{name}: h needs a residual")
+    x, ldx = _norm_rows(x, f"{name}: x")
+    rows, cols = x.shape
+    _norm_cols(cols, name)
+    if quant and cols % group:
+        raise ValueError(f"{name}: cols ({cols}) must be a multiple of the group ({group})")
+    weight = _norm_weight(weight, cols, name)
+    ldr = ldh = ldy = cols
+    if residual is not None:
+        residual, ldr = _norm_rows(residual, f"{name}: residual", x.shape)
+        if h is not None:
+            ldh = _norm_out(h, f"{name}: h", x.shape, residual.dtype)
+    dev = _check_dev(x, weight, residual, h)
+    if residual is not None and h is None:
+        h = torch.empty(rows, cols, dtype=residual.dtype, device=dev)
+    y = q = s = None
+    if y_dtype is not None:
+        y = torch.empty(rows, cols, dtype=_out_dtype(y_dtype, name), device=dev)
+    if quant:
+        q = torch.empty(rows, cols, dtype=_U8, device=dev)
+        s = torch.empty(rows, cols // group, dtype=_U8, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _call_on(dev, name, x.data_ptr(), _dtype_code(x), rows, cols, ldx, _ptr(residual),
+             F32 if residual is None else _dtype_code(residual), ldr, weight.data_ptr(), _dtype_code(weight), eps, group,
+             _ptr(h), ldh, rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _dtype_code(y), ldy,
+             _stream(x))
+    return q, s, y, x if h is None else h, rstd
+
+
+def rmsnorm_backward_workspace_size(rows, cols):
+    return int(_lib.rmsnorm_backward_workspace_size(rows, cols))
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
+    """Gradient of rmsnorm_quant's y: dy [rows, cols], h and rstd of the forward -> (dx [rows, cols] in h's dtype,
+    dweight fp32 [cols]).
+
+    dx is the gradient of h, and so of x and the residual, with dh (what reaches h past the norm, in h's dtype) added
+    before its rounding; dx= takes a tensor for it, which may be dh or dy itself."""
+    name = "rmsnorm_backward"
+    dy, lddy = _norm_rows(dy, f"{name}: dy")
+    rows, cols = dy.shape
+    _norm_cols(cols, name)
+    h, ldh = _norm_rows(h, f"{name}: h", dy.shape)
+    weight = _norm_weight(weight, cols, name)
+    _need(rstd, f"{name}: rstd", shape=(rows,), dtype=torch.float32, contiguous=True)
+    lddh = lddx = cols
+    if dh is not None:
+        _need(dh, f"{name}: dh", dtype=h.dtype)
+        dh, lddh = _norm_rows(dh, f"{name}: dh", dy.shape)
+    if dx is not None:
+        lddx = _norm_out(dx, f"{name}: dx", dy.shape, h.dtype)
+    if workspace is not None:
+        _need(workspace, f"{name}: workspace", dtype=_U8, contiguous=True)
+    dev = _check_dev(dy, h, weight, rstd, dh, dx, workspace)
+    if dx is None:
+        dx = torch.empty(rows, cols, dtype=h.dtype, device=dev)
+    if workspace is None:
+        workspace = torch.empty(_lib.rmsnorm_backward_workspace_size(rows, cols), dtype=_U8, device=dev)
+    dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    _call_on(dev, name, dy.data_ptr(), _dtype_code(dy), rows, cols, lddy, h.data_ptr(), _dtype_code(h), ldh,
+             weight.data_ptr(), _dtype_code(weight), rstd.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), lddx,
+             dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dy))
+    return dx, dweight
+
+
+# ---------------------------------------------------------------------------
+def _grad_list(grads, name, what="gradient"):
+    """Checks of a list of gradients: (n, pointers, lengths, type codes, device)."""
+    dev = None
+    for i, g in enumerate(grads):
+        if not g.is_cuda:
+            raise ValueError("all tensors must be on the GPU")
+        if dev is None:
+            dev = g.device
+        elif g.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        if not g.is_contiguous():
+            raise ValueError(f"{name}: {what} {i} must be contiguous")
+    if dev is None:
+        raise ValueError(f"{name}: the list is empty")
+    n = len(grads)
+    return (n, (C.c_void_p * n)(*[g.data_ptr() for g in grads]), (C.c_int64 * n)(*[g.numel() for g in grads]),
+            (C.c_int * n)(*[_dtype_code(g) for g in grads]), dev)
+
+
+def grad_sumsq_workspace_size(numel):
+    """Bytes that grad_sumsq and grad_clip need for gradients of these lengths."""
+    return int(_lib.grad_sumsq_workspace_size((C.c_int64 * len(numel))(*numel), len(numel)))
+
+
+def _grad_workspace(workspace, numel, n, dev, name):
+    if workspace is None:
+        return torch.empty(_lib.grad_sumsq_workspace_size(numel, n), dtype=_U8, device=dev)
+    return _need(workspace, f"{name}: workspace", dtype=_U8, contiguous=True)
+
+
+def _grad_scalar(t, name, dev):
+    _need(t, name, dtype=torch.float64)
+    if t.numel() != 1 or t.device != dev:
+        raise ValueError(f"{name} must hold one value on the gradients' GPU")
+    return t
+
+
+def grad_sumsq(grads, out=None, accumulate=False, workspace=None):
+    """Sum of the squares of all elements of a list of gradients (fp32/bf16, contiguous) -> out fp64 scalar tensor;
+    accumulate: added to what out holds.  Summed over ranks, it is grad_clip's sumsq."""
+    name = "grad_sumsq"
+    grads = list(grads)
+    n, ptrs, numel, types, dev = _grad_list(grads, name)
+    if accumulate and out is None:
+        raise ValueError(f"{name}: accumulate needs out")
+    if out is not None:
+        _grad_scalar(out, f"{name}: out", dev)
+    workspace = _grad_workspace(workspace, numel, n, dev, name)
+    _check_dev(grads[0], workspace)
+    if out is None:
+        out = torch.empty((), dtype=torch.float64, device=dev)
+    _call_on(dev, name, ptrs, numel, types, n, out.data_ptr(), 1 if accumulate else 0, workspace.data_ptr(),
+             workspace.numel(), _stream(out))
+    return out
+
+
+def grad_clip(grads, max_norm, scale=1.0, out=None, sumsq=None, workspace=None):
+    """Clips a list of gradients (fp32/bf16, contiguous) to the global norm max_norm: -> norm fp32 scalar tensor.
+
+    norm = scale * sqrt(sum of squares); each gradient times scale * min(1, max_norm / norm) is written to out (a list
+    of tensors of the same lengths, fp32/bf16; None: in place).  sumsq: fp64, in place of these gradients' own sum of
+    squares (grad_sumsq's, summed over ranks).  An infinite or NaN norm clips nothing."""
+    name = "grad_clip"
+    grads = list(grads)
+    n, ptrs, numel, types, dev = _grad_list(grads, name)
+    if not (max_norm > 0 and 0 < scale < float("inf")):
+        raise ValueError(f"{name}: max_norm and scale must be positive")
+    optrs, otypes = ptrs, types
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError(f"{name}: out must hold {n} tensors, got {len(out)}")
+        _, optrs, olen, otypes, odev = _grad_list(out, name, "output")
+        if odev != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        for i in range(n):
+            if olen[i] != numel[i]:
+                raise ValueError(f"{name}: output {i} must hold {numel[i]} elements, got {olen[i]}")
+    if sumsq is not None:
+        _grad_scalar(sumsq, f"{name}: sumsq", dev)
+    else:
+        workspace = _grad_workspace(workspace, numel, n, dev, name)
+        _check_dev(grads[0], workspace)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    _call_on(dev, name, ptrs, optrs, numel, types, otypes, n, max_norm, scale, _ptr(sumsq), norm.data_ptr(),
+             _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(norm))
+    return norm

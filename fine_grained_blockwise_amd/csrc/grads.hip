@@ -1,0 +1,365 @@
+// grads.hip -- the global norm of many gradients, and their clipping.
+//
+//   S = sum over all tensors of g^2, norm = scale sqrt(S),
+//   out = g scale min(1, max_norm / norm); a norm that is infinite or NaN clips nothing.
+//
+// Squares and sums are FP64: each square of a BF16 or FP32 value is exact to 2^-53 and none
+// over- or underflows.  Every sum has a fixed order: a workgroup's chunks, its threads, then
+// the workgroups.
+//
+// Bound by memory: the gradients are read twice, the clipped ones written once.  The
+// tensors' addresses travel in the kernel's arguments (4 KB hold LIST of them), so that a
+// captured launch has them and nothing is copied; a longer list takes several launches.
+#include <algorithm>
+
+#include "fgb_internal.h"
+
+namespace fgb {
+
+constexpr int LIST = 120;       // tensors of one launch
+constexpr int CHUNK = 16384;    // elements a workgroup takes at a time, of one tensor
+constexpr int MOST_GRID = 2048; // workgroups of one launch
+
+struct GradList {
+    const void *p[LIST];
+    void *o[LIST];
+    int64_t n[LIST];      // elements
+    uint32_t upto[LIST];  // chunks of this and the tensors before
+    uint8_t bf16[LIST];   // bit 0: the gradient is BF16, bit 1: the output
+    int count;
+};
+static_assert(sizeof(GradList) <= 3712, "the arguments of a launch are at most 4 KB");
+
+// The tensor that chunk c belongs to.
+__device__ __forceinline__ int tensor_of(const GradList &l, uint32_t c)
+{
+    int lo = 0, hi = l.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (c < l.upto[mid])
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// Eight neighbouring gradients (the addresses are aligned to one element only: the card's
+// loads and stores need no more).
+template <bool BF16> __device__ __forceinline__ void load8g(const void *p, int64_t at, float (&f)[8])
+{
+    if constexpr (BF16) {
+        uint32_t u[4];
+        __builtin_memcpy(u, (const uint16_t *)p + at, 16);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            f[2 * i] = bf16lo(u[i]);
+            f[2 * i + 1] = bf16hi(u[i]);
+        }
+    } else {
+        __builtin_memcpy(f, (const float *)p + at, 32);
+    }
+}
+template <bool BF16> __device__ __forceinline__ float load1g(const void *p, int64_t at)
+{
+    return BF16 ? __uint_as_float((uint32_t)((const uint16_t *)p)[at] << 16) : ((const float *)p)[at];
+}
+template <bool BF16> __device__ __forceinline__ void store8g(void *p, int64_t at, const float (&f)[8])
+{
+    if constexpr (BF16) {
+        const uint32_t u[4] = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                               pack_bf16x2(f[6], f[7])};
+        __builtin_memcpy((uint16_t *)p + at, u, 16);
+    } else {
+        __builtin_memcpy((float *)p + at, f, 32);
+    }
+}
+template <bool BF16> __device__ __forceinline__ void store1g(void *p, int64_t at, float f)
+{
+    if constexpr (BF16)
+        ((__bf16 *)p)[at] = (__bf16)f;
+    else
+        ((float *)p)[at] = f;
+}
+
+template <bool BF16> __device__ __forceinline__ double chunk_squares(const void *p, int64_t from, int64_t to)
+{
+    double sum = 0.0;
+    const int64_t whole = from + (to - from) / 8 * 8;
+    for (int64_t i = from + 8 * threadIdx.x; i < whole; i += 8 * 256) {
+        float f[8];
+        load8g<BF16>(p, i, f);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            sum = fma((double)f[j], (double)f[j], sum);
+    }
+    if (whole + threadIdx.x < to) {
+        const double v = load1g<BF16>(p, whole + threadIdx.x);
+        sum = fma(v, v, sum);
+    }
+    return sum;
+}
+
+// The workgroup's sum of v, in thread 0.
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double red[4];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        v += __shfl_xor(v, d);
+    if (lane_id() == 0)
+        red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return red[0] + red[1] + red[2] + red[3];
+}
+
+__global__ __launch_bounds__(256) void grad_squares_kernel(GradList l, double *part)
+{
+    double sum = 0.0;
+    const uint32_t chunks = l.upto[l.count - 1];
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int t = tensor_of(l, c);
+        const int64_t from = (int64_t)(c - (t ? l.upto[t - 1] : 0u)) * CHUNK;
+        const int64_t to = from + CHUNK < l.n[t] ? from + CHUNK : l.n[t];
+        sum += l.bf16[t] & 1 ? chunk_squares<true>(l.p[t], from, to) : chunk_squares<false>(l.p[t], from, to);
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = sum;
+}
+
+__global__ __launch_bounds__(256) void grad_total_kernel(const double *part, int n, double *out, int accumulate)
+{
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < n; i += 256)
+        sum += part[i];
+    sum = block_sum(sum);
+    if (threadIdx.x == 0)
+        *out = accumulate ? *out + sum : sum;
+}
+
+template <bool IN, bool OUT>
+__device__ __forceinline__ void chunk_scale(const void *p, void *o, int64_t from, int64_t to, float f)
+{
+    const int64_t whole = from + (to - from) / 8 * 8;
+    for (int64_t i = from + 8 * threadIdx.x; i < whole; i += 8 * 256) {
+        float v[8];
+        load8g<IN>(p, i, v);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[j] *= f;
+        store8g<OUT>(o, i, v);
+    }
+    if (whole + threadIdx.x < to)
+        store1g<OUT>(o, whole + threadIdx.x, load1g<IN>(p, whole + threadIdx.x) * f);
+}
+
+// The last chunks first: they are the ones that the sums' pass left in the cache.
+__global__ __launch_bounds__(256) void grad_scale_kernel(GradList l, const double *squares, double max_norm,
+                                                         double scale, float *norm_out)
+{
+    const double norm = scale * sqrt(*squares);
+    const bool clip = norm > max_norm && norm < __builtin_inf();
+    const float f = (float)(clip ? scale * (max_norm / norm) : scale);
+    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0)
+        *norm_out = (float)norm;
+    if (l.count == 0)
+        return;
+    const uint32_t chunks = l.upto[l.count - 1];
+    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const uint32_t c = chunks - 1 - k;
+        const int t = tensor_of(l, c);
+        const int kind = l.bf16[t];
+        if (f == 1.0f && l.p[t] == l.o[t])
+            continue; // in place and unchanged
+        const int64_t from = (int64_t)(c - (t ? l.upto[t - 1] : 0u)) * CHUNK;
+        const int64_t to = from + CHUNK < l.n[t] ? from + CHUNK : l.n[t];
+        if (kind == 3)
+            chunk_scale<true, true>(l.p[t], l.o[t], from, to, f);
+        else if (kind == 2)
+            chunk_scale<false, true>(l.p[t], l.o[t], from, to, f);
+        else if (kind == 1)
+            chunk_scale<true, false>(l.p[t], l.o[t], from, to, f);
+        else
+            chunk_scale<false, false>(l.p[t], l.o[t], from, to, f);
+    }
+}
+
+static unsigned grad_grid(const GradList &l)
+{
+    const uint32_t chunks = l.count ? l.upto[l.count - 1] : 1;
+    return chunks < MOST_GRID ? chunks : MOST_GRID;
+}
+
+static int64_t chunks_of(int64_t n) { return (n + CHUNK - 1) / CHUNK; }
+
+// The tensors from `at` on that one launch takes; empty ones are passed over.
+static int next_list(GradList &l, int at, int n, const void *const *grads, void *const *outs, const int64_t *numel,
+                     const int *dtypes, const int *out_dtypes)
+{
+    l.count = 0;
+    uint32_t upto = 0;
+    for (; at < n && l.count < LIST; at++) {
+        if (numel[at] == 0)
+            continue;
+        const int k = l.count++;
+        l.p[k] = grads[at];
+        l.o[k] = outs ? outs[at] : nullptr;
+        l.n[k] = numel[at];
+        l.upto[k] = upto += (uint32_t)chunks_of(numel[at]);
+        l.bf16[k] = (dtypes[at] == FGB_BF16 ? 1 : 0) | (outs && out_dtypes[at] == FGB_BF16 ? 2 : 0);
+    }
+    return at;
+}
+
+static int check_grads(const char *name, int n, const void *const *grads, const int64_t *numel, const int *dtypes)
+{
+    FGB_REQUIRE(n >= 0 && (n == 0 || (grads && numel && dtypes)), FGB_EINVAL, "%s: null list", name);
+    int64_t chunks = 0;
+    for (int i = 0; i < n; i++) {
+        FGB_REQUIRE(dtypes[i] == FGB_F32 || dtypes[i] == FGB_BF16, FGB_EUNSUPPORTED,
+                    "%s: gradient %d must be FGB_F32 or FGB_BF16", name, i);
+        FGB_REQUIRE(numel[i] >= 0 && numel[i] < (1ll << 40), FGB_EINVAL, "%s: gradient %d has a bad length", name, i);
+        FGB_REQUIRE(numel[i] == 0 || (grads[i] && ((uintptr_t)grads[i] & (dtypes[i] == FGB_BF16 ? 1 : 3)) == 0),
+                    FGB_EINVAL, "%s: gradient %d is null or misaligned", name, i);
+        chunks += chunks_of(numel[i]);
+    }
+    FGB_REQUIRE(chunks < (1ll << 31), FGB_EINVAL, "%s: too many elements", name);
+    return FGB_OK;
+}
+
+// No output may lie over another one, or over a gradient that is not its own.
+static bool outputs_overlap(int n, const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
+                            const int *out_dtypes)
+{
+    struct Span {
+        uintptr_t from, to;
+        int of, out;
+    };
+    Span *const spans = new (std::nothrow) Span[2 * (size_t)n];
+    if (!spans)
+        return true;
+    int m = 0;
+    for (int i = 0; i < n; i++) {
+        if (numel[i] == 0)
+            continue;
+        const uintptr_t p = (uintptr_t)grads[i], o = (uintptr_t)outs[i];
+        if (!(p == o && dtypes[i] == out_dtypes[i])) // in place: one span for both
+            spans[m++] = {p, p + (size_t)numel[i] * (dtypes[i] == FGB_BF16 ? 2 : 4), i, 0};
+        spans[m++] = {o, o + (size_t)numel[i] * (out_dtypes[i] == FGB_BF16 ? 2 : 4), i, 1};
+    }
+    std::sort(spans, spans + m, [](const Span &a, const Span &b) { return a.from < b.from; });
+    bool bad = false;
+    uintptr_t out_end = 0, any_end = 0; // ends of the outputs and of all spans so far
+    for (int i = 0; i < m && !bad; i++) {
+        bad = spans[i].from < (spans[i].out ? any_end : out_end);
+        any_end = std::max(any_end, spans[i].to);
+        if (spans[i].out)
+            out_end = std::max(out_end, spans[i].to);
+    }
+    delete[] spans;
+    return bad;
+}
+
+// Partial sums of all launches of a list: its non-empty tensors in runs of LIST.
+static int64_t partials(int n, const int64_t *numel)
+{
+    int64_t total = 0, chunks = 0;
+    int count = 0;
+    for (int i = 0; i < n; i++) {
+        if (numel[i] <= 0)
+            continue;
+        chunks += chunks_of(numel[i]);
+        if (++count == LIST) {
+            total += chunks < MOST_GRID ? chunks : MOST_GRID;
+            chunks = count = 0;
+        }
+    }
+    return total + (chunks < MOST_GRID ? chunks : MOST_GRID);
+}
+
+static int sum_squares(int n, const void *const *grads, const int64_t *numel, const int *dtypes, double *part,
+                       double *out, int accumulate, hipStream_t st)
+{
+    GradList l;
+    int64_t done = 0;
+    for (int at = 0; at < n;) {
+        at = next_list(l, at, n, grads, nullptr, numel, dtypes, nullptr);
+        if (l.count == 0)
+            break;
+        const unsigned grid = grad_grid(l);
+        grad_squares_kernel<<<grid, 256, 0, st>>>(l, part + done);
+        FGB_LAUNCHED("grad_squares_kernel");
+        done += grid;
+    }
+    grad_total_kernel<<<1, 256, 0, st>>>(part, (int)done, out, accumulate);
+    FGB_LAUNCHED("grad_total_kernel");
+    return FGB_OK;
+}
+
+} // namespace fgb
+
+using namespace fgb;
+
+extern "C" size_t grad_sumsq_workspace_size(const int64_t *numel, int n)
+{
+    return n < 0 || (n > 0 && !numel) ? 0 : 8 * (size_t)(partials(n, numel) + 1);
+}
+
+extern "C" int grad_sumsq(const void *const *grads, const int64_t *numel, const int *dtypes, int n, double *sumsq,
+                          int accumulate, void *workspace, size_t ws_bytes, void *stream)
+{
+    clear_error();
+    const int rc = check_grads("grad_sumsq", n, grads, numel, dtypes);
+    if (rc != FGB_OK)
+        return rc;
+    FGB_REQUIRE(sumsq && ((uintptr_t)sumsq & 7) == 0, FGB_EINVAL, "grad_sumsq: sumsq null or misaligned");
+    const size_t need = grad_sumsq_workspace_size(numel, n);
+    FGB_REQUIRE(workspace && ws_bytes >= need, FGB_EWORKSPACE, "grad_sumsq: workspace of %zu bytes needed", need);
+    FGB_REQUIRE(((uintptr_t)workspace & 7) == 0, FGB_EINVAL, "grad_sumsq: workspace must be 8-byte aligned");
+    return sum_squares(n, grads, numel, dtypes, (double *)workspace, sumsq, accumulate, (hipStream_t)stream);
+}
+
+extern "C" int grad_clip(const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
+                         const int *out_dtypes, int n, double max_norm, double scale, const double *sumsq, float *norm,
+                         void *workspace, size_t ws_bytes, void *stream)
+{
+    clear_error();
+    int rc = check_grads("grad_clip", n, grads, numel, dtypes);
+    if (rc != FGB_OK)
+        return rc;
+    FGB_REQUIRE(n == 0 || (outs && out_dtypes), FGB_EINVAL, "grad_clip: null list");
+    for (int i = 0; i < n; i++) {
+        FGB_REQUIRE(out_dtypes[i] == FGB_F32 || out_dtypes[i] == FGB_BF16, FGB_EUNSUPPORTED,
+                    "grad_clip: output %d must be FGB_F32 or FGB_BF16", i);
+        FGB_REQUIRE(numel[i] == 0 || (outs[i] && ((uintptr_t)outs[i] & (out_dtypes[i] == FGB_BF16 ? 1 : 3)) == 0),
+                    FGB_EINVAL, "grad_clip: output %d is null or misaligned", i);
+    }
+    FGB_REQUIRE(max_norm > 0.0 && scale > 0.0 && scale < __builtin_inf(), FGB_EINVAL,
+                "grad_clip: max_norm and scale must be positive");
+    FGB_REQUIRE(!outputs_overlap(n, grads, outs, numel, dtypes, out_dtypes), FGB_EINVAL,
+                "grad_clip: an output lies over another one or over a gradient that is not its own");
+    FGB_REQUIRE(((uintptr_t)sumsq & 7) == 0 && norm && ((uintptr_t)norm & 3) == 0, FGB_EINVAL,
+                "grad_clip: sumsq misaligned, or norm null or misaligned");
+    const hipStream_t st = (hipStream_t)stream;
+    if (!sumsq) {
+        const size_t need = grad_sumsq_workspace_size(numel, n);
+        FGB_REQUIRE(workspace && ws_bytes >= need, FGB_EWORKSPACE, "grad_clip: workspace of %zu bytes needed", need);
+        FGB_REQUIRE(((uintptr_t)workspace & 7) == 0, FGB_EINVAL, "grad_clip: workspace must be 8-byte aligned");
+        double *total = (double *)workspace;
+        if ((rc = sum_squares(n, grads, numel, dtypes, total + 1, total, 0, st)) != FGB_OK)
+            return rc;
+        sumsq = total;
+    }
+    GradList l;
+    int at = 0;
+    do { // (an empty list still gives the norm)
+        at = next_list(l, at, n, grads, outs, numel, dtypes, out_dtypes);
+        if (l.count == 0 && norm == nullptr)
+            break;
+        grad_scale_kernel<<<grad_grid(l), 256, 0, st>>>(l, sumsq, max_norm, scale, norm);
+        FGB_LAUNCHED("grad_scale_kernel");
+        norm = nullptr;
+    } while (at < n);
+    return FGB_OK;
+}

@@ -706,6 +706,101 @@ int moe_router_backward(const void *logits, int dtype, int64_t T, int E, int64_t
                         const int32_t *counts, const float *dweights, const float *dloss, int score, int renorm,
                         float scale, float loss_coef, void *dlogits, int64_t ldd, void *stream);
 
+/*
+ * moe_router_grouped -- moe_router with a choice that a bias and groups of experts
+ * decide; the weights, counts and loss are those of the scores s and p as before.
+ *   bias         [E] FP32 or NULL: experts are chosen by c = s + bias, s rounded to FP32
+ *                (to nearest) and the sum once more; without a bias by the logits
+ *   groups, topk_groups : the experts are `groups` runs of E / groups (1 <= groups <= 64,
+ *                dividing E).  A group's value is the sum of its two largest c (of its only
+ *                one where just one can be chosen) with a bias, its largest logit without.
+ *                Experts are chosen from the topk_groups groups of largest value only
+ *                (1 <= topk_groups <= groups, topk <= topk_groups * E / groups)
+ *   topk_idx[t]  the experts of the topk largest c (logits), largest first; equal values,
+ *                of groups too: the lowest id.  A logit or a c of -inf or NaN is never
+ *                chosen; a token is live if it is not masked and has an expert that can be.
+ * Other arguments, and the workspace, as for moe_router.  moe_router_backward gives the
+ * gradient: the choice, and with it the bias, are constants of it.
+ */
+int moe_router_grouped(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk, const uint8_t *token_mask,
+                       const float *bias, int groups, int topk_groups, int score, int renorm, float scale,
+                       float loss_coef, int32_t *topk_idx, float *weights, int32_t *counts, float *loss,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * moe_bias_update -- the bias for the next step: out[e] = bias[e] + rate where counts[e] is
+ * below the mean of counts[0 .. E), - rate above it, bias[e] at it.  out may be bias.
+ */
+int moe_bias_update(const float *bias, const int32_t *counts, int E, float rate, float *out, void *stream);
+
+/*
+ * rmsnorm_quant -- RMSNorm with the residual's addition, written as the E4M3 codes and
+ * scales that the products and permute_pad read (swiglu_quant's twin for the first product).
+ *   h = x + residual, the FP32 sum rounded to the residual's type; h = x without a residual
+ *   rstd = 1 / sqrt(mean over the columns of h^2 + eps), y = h * rstd * weight (FP32)
+ *   x        [rows, cols], row stride ldx, FGB_F32 or FGB_BF16; cols % 32 == 0, cols <= 32768
+ *   residual [rows, cols], row stride ldr, either type; NULL: none (h, ldh are then unused)
+ *   weight   [cols], either type; eps > 0; group 128 or 32
+ *   h        [rows, cols], row stride ldh, in the residual's type: the new residual stream.
+ *            It may be the residual itself (or, of the same type, x); no other overlap
+ *   rstd     [rows] FP32, for rmsnorm_backward
+ *   q, s     [rows, cols] codes and [rows, cols / group] scales, dense (cols % group == 0), of
+ *            the FP32 y as fp8_quant_rowwise gives them; both NULL: not wanted
+ *   y        [rows, cols], row stride ldy, y in y_dtype (BF16: nearest even); NULL: not wanted.
+ *            (Codes or y have to be.)
+ * The sum of squares is FP32: it has to be in that range.
+ */
+int rmsnorm_quant(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
+                  int r_dtype, int64_t ldr, const void *weight, int w_dtype, float eps, int group, void *h, int64_t ldh,
+                  float *rstd, uint8_t *q, uint8_t *s, void *y, int y_dtype, int64_t ldy, void *stream);
+
+/*
+ * rmsnorm_backward -- the gradient of rmsnorm_quant's y.  With a = dy * weight and
+ * hat = h * rstd:
+ *   dx      = dh + rstd * (a - hat * mean over the columns of a * hat), rounded once; [rows,
+ *             cols], row stride lddx, in h's type: the gradient of h, thus of x and residual
+ *   dweight = sum over the rows of dy * hat; [cols] FP32
+ *   dy  [rows, cols], row stride lddy, either type; h, rstd: the forward's (x, without a
+ *       residual); dh [rows, cols], row stride lddh, in h's type: the gradient that reaches h
+ *       past the norm; NULL: 0.  dx may be dy (of the same type) or dh itself
+ *   workspace: rmsnorm_backward_workspace_size(rows, cols) bytes, contents on entry irrelevant.
+ * rows = 0 gives a dweight of zeros.
+ */
+int rmsnorm_backward(const void *dy, int dy_dtype, int64_t rows, int64_t cols, int64_t lddy, const void *h, int h_dtype,
+                     int64_t ldh, const void *weight, int w_dtype, const float *rstd, const void *dh, int64_t lddh,
+                     void *dx, int64_t lddx, float *dweight, void *workspace, size_t ws_bytes, void *stream);
+size_t rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * grad_sumsq -- the sum of the squares of n gradients' elements, in FP64 throughout.
+ *   grads, numel, dtypes : host arrays of n device pointers (aligned to their element),
+ *               lengths (0 is allowed) and types (FGB_F32 or FGB_BF16), read before the call
+ *               returns
+ *   sumsq       device double; accumulate != 0: added to what it holds (so that ranks or
+ *               several lists add up)
+ *   workspace   grad_sumsq_workspace_size(numel, n) bytes, 8-byte aligned, contents irrelevant
+ */
+int grad_sumsq(const void *const *grads, const int64_t *numel, const int *dtypes, int n, double *sumsq, int accumulate,
+               void *workspace, size_t ws_bytes, void *stream);
+size_t grad_sumsq_workspace_size(const int64_t *numel, int n);
+
+/*
+ * grad_clip -- the global norm of n gradients, and their clipping to it.
+ *   norm = scale * sqrt(sum of squares), out = grad * scale * min(1, max_norm / norm), the
+ *   factor rounded to FP32 and the product once to the output's type.  A norm that is
+ *   infinite or NaN clips nothing (out = grad * scale); the caller sees it in `norm`.
+ *   grads, numel, dtypes : as for grad_sumsq; outs, out_dtypes: where the clipped gradients
+ *               go, each in its own type.  An output may be its gradient itself (of the same
+ *               type), and may lie over nothing else of the list
+ *   max_norm, scale > 0 (scale: what the gradients are still to be multiplied with)
+ *   sumsq       device double: the sum of squares, as grad_sumsq gave it (and other ranks
+ *               added to it); NULL: of these gradients, then with the workspace of grad_sumsq
+ *   norm        device float
+ */
+int grad_clip(const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
+              const int *out_dtypes, int n, double max_norm, double scale, const double *sumsq, float *norm,
+              void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

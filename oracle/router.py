@@ -15,6 +15,39 @@ def select(z, k, mask=None):
     return np.where(ok, idx, -1).astype(np.int32)
 
 
+def choose(z, k, score=SOFTMAX, bias=None, groups=1, topk_groups=1, mask=None):
+    """Ids [T, k] where a bias and groups decide: the k largest c (ties: lowest id) in the topk_groups groups of
+    largest value.  c = FP32(FP32(s) + bias), or the logits without a bias."""
+    z = np.asarray(z, np.float64)
+    T, E = z.shape
+    c = np.where(z > -np.inf, z, -np.inf)  # NaN too
+    if bias is not None:
+        for t in range(T):
+            ok = c[t] > -np.inf
+            with np.errstate(all="ignore"):
+                if score == SOFTMAX:
+                    top = z[t, ok].max(initial=-np.inf)
+                    s = np.where(z[t, ok] == top, 1.0, np.exp(z[t, ok] - top))
+                    s = s / s.sum() if s.size else s
+                else:
+                    s = 1 / (1 + np.exp(-z[t, ok]))
+                v = s.astype(np.float32) + np.asarray(bias, np.float32)[ok]
+            c[t, ok] = np.where(np.isnan(v), -np.inf, v)
+    if groups > 1:
+        part = -np.sort(-c.reshape(T, groups, E // groups), axis=2)
+        value = part[:, :, 0].copy()
+        if bias is not None and E // groups > 1:
+            second = part[:, :, 1]
+            with np.errstate(all="ignore"):
+                both = value.astype(np.float32) + second.astype(np.float32)
+            value = np.where(second > -np.inf, both, value)
+        best = np.argsort(-value, axis=1, kind="stable")[:, :topk_groups]
+        shut = np.ones((T, groups), bool)
+        np.put_along_axis(shut, best, False, 1)
+        c = np.where(np.repeat(shut, E // groups, 1), -np.inf, c)
+    return select(c, k, mask)
+
+
 def scores(z, score):
     """(s, p) of rows with at least one usable logit."""
     with np.errstate(all="ignore"):
@@ -32,11 +65,11 @@ def log_sigmoid(z):
         return np.minimum(z, 0) - np.log1p(np.exp(-np.abs(z)))
 
 
-def forward(z, k, score=SOFTMAX, renorm=False, scale=1.0, coef=0.0, mask=None):
-    """-> dict(idx, weights, counts [E + 1], loss)."""
+def forward(z, k, score=SOFTMAX, renorm=False, scale=1.0, coef=0.0, mask=None, idx=None):
+    """-> dict(idx, weights, counts [E + 1], loss); idx: the choice, where it is not select()'s."""
     z = np.asarray(z, np.float64)
     T, E = z.shape
-    idx = select(z, k, mask)
+    idx = select(z, k, mask) if idx is None else idx
     live = (idx >= 0).any(1)
     weights, psum = np.zeros((T, k)), np.zeros(E)
     for t in np.flatnonzero(live):

@@ -75,9 +75,9 @@ template <bool BF16> __device__ __forceinline__ Raw8<BF16> narrow(const float (&
 template <bool BF16> __device__ __forceinline__ void store8(void *p, int64_t at, const Raw8<BF16> &o)
 {
     uint8_t *b = (uint8_t *)p + at * (BF16 ? 2 : 4);
-    st_stream16(b, o.v[0]);
+    st_plain16(b, o.v[0]);
     if constexpr (!BF16)
-        st_stream16(b + 16, o.v[1]);
+        st_plain16(b + 16, o.v[1]);
 }
 __device__ __forceinline__ void load_weight(const void *w, int bf16, int64_t at, float (&f)[8])
 {
@@ -118,35 +118,52 @@ template <int W> __device__ __forceinline__ float row_sum(float v, float *red)
 template <int W> constexpr int NORM_THREADS = W == 1 ? 256 : 64 * W;
 template <int W> constexpr int NORM_ROWS = W == 1 ? 4 : 1; // rows of a workgroup at a time
 
+// Chunk u's first column in this lane, and where it is loaded from: lanes past the last
+// column load the last chunk once more, so that the loads of a row are issued together.
+template <int W> __device__ __forceinline__ int chunk_col(int u, int t) { return 8 * (u * 64 * W + t); }
+template <bool BF16, int W, int CH>
+__device__ __forceinline__ void load_row(Raw8<BF16> (&o)[CH], const void *p, int64_t at, int cols, int t)
+{
+#pragma unroll
+    for (int u = 0; u < CH; u++)
+        o[u] = load8<BF16>(p, at + min(chunk_col<W>(u, t), cols - 8));
+}
+
 template <bool XBF, bool HBF, bool RES, int W, int CH>
 __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_kernel(NormArgs a)
 {
     __shared__ float red[2][16];
     const int t = threadIdx.x % (64 * W); // lane of the row
     int odd = 0;
-    for (int64_t row = (int64_t)blockIdx.x * NORM_ROWS<W> + (W == 1 ? threadIdx.x >> 6 : 0); row < a.rows;
-         row += (int64_t)gridDim.x * NORM_ROWS<W>) {
+    const int64_t first = (int64_t)blockIdx.x * NORM_ROWS<W> + (W == 1 ? threadIdx.x >> 6 : 0);
+    Raw8<XBF> x[CH];
+    Raw8<HBF> r[CH];
+    for (int64_t row = first; row < a.rows; row += (int64_t)gridDim.x * NORM_ROWS<W>) {
+        load_row<XBF, W>(x, a.x, row * a.ldx, a.cols, t);
+        if constexpr (RES)
+            load_row<HBF, W>(r, a.r, row * a.ldr, a.cols, t);
         float f[CH][8];
         float sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < CH; u++) {
-            const int c = 8 * (u * 64 * W + t);
-            if (c < a.cols) {
-                widen<XBF>(load8<XBF>(a.x, row * a.ldx + c), f[u]);
-                if constexpr (RES) {
-                    float r[8];
-                    widen<HBF>(load8<HBF>(a.r, row * a.ldr + c), r);
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        r[i] = f[u][i] + r[i];
-                    const Raw8<HBF> h = narrow<HBF>(r); // the norm is that of the stream as it is stored
-                    store8<HBF>(a.h, row * a.ldh + c, h);
-                    widen<HBF>(h, f[u]);
-                }
+            const int c = chunk_col<W>(u, t);
+            widen<XBF>(x[u], f[u]);
+            if constexpr (RES) {
+                float v[8];
+                widen<HBF>(r[u], v);
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    sum += f[u][i] * f[u][i];
+                    v[i] = f[u][i] + v[i];
+                const Raw8<HBF> h = narrow<HBF>(v); // the norm is that of the stream as it is stored
+                if (c < a.cols)
+                    store8<HBF>(a.h, row * a.ldh + c, h);
+                widen<HBF>(h, f[u]);
             }
+            float part = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                part = fmaf(f[u][i], f[u][i], part);
+            sum += c < a.cols ? part : 0.0f;
         }
         sum = row_sum<W>(sum, red[odd]);
         odd ^= 1;
@@ -155,7 +172,7 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_kernel(NormArgs a)
             a.rstd[row] = rstd;
 #pragma unroll
         for (int u = 0; u < CH; u++) {
-            const int c = 8 * (u * 64 * W + t);
+            const int c = chunk_col<W>(u, t);
             if (c < a.cols) { // (whole groups of lanes: cols is a multiple of the group)
                 float w[8], y[8];
                 load_weight(a.w, a.w_bf16, c, w);
@@ -181,7 +198,7 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_kernel(NormArgs a)
                     const float sc = pow2f(-e);
                     const uint2 o = make_uint2(cvt4_e4m3(y[0] * sc, y[1] * sc, y[2] * sc, y[3] * sc),
                                                cvt4_e4m3(y[4] * sc, y[5] * sc, y[6] * sc, y[7] * sc));
-                    st_stream8(a.q + row * a.cols + c, o);
+                    *reinterpret_cast<uint2 *>(a.q + row * a.cols + c) = o;
                     if (c % a.group == 0)
                         a.s[row * (a.cols / a.group) + c / a.group] = (uint8_t)(e + 127);
                 }
@@ -196,61 +213,63 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_grad_kernel(NormGradA
     __shared__ float red[2][16];
     const int t = threadIdx.x % (64 * W);
     const int64_t first = (int64_t)blockIdx.x * NORM_ROWS<W> + (W == 1 ? threadIdx.x >> 6 : 0);
+    if (W == 1 && first >= a.parts) // (a whole wave, and no barrier follows)
+        return;
     float w[CH][8], dw[CH][8];
+    Raw8<DBF> rd[CH];
+    Raw8<HBF> rh[CH], re[CH];
 #pragma unroll
     for (int u = 0; u < CH; u++) {
-        const int c = 8 * (u * 64 * W + t);
+        const int c = chunk_col<W>(u, t);
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            w[u][i] = dw[u][i] = 0.0f;
+            w[u][i] = dw[u][i] = 0.0f; // (columns past the last one add nothing)
         if (c < a.cols)
             load_weight(a.w, a.w_bf16, c, w[u]);
     }
     int odd = 0;
-    for (int64_t row = first < a.parts ? first : a.rows; row < a.rows; row += a.parts) {
-        float d[CH][8], h[CH][8];
+    for (int64_t row = first; row < a.rows; row += a.parts) {
         const float rstd = a.rstd[row];
+        load_row<DBF, W>(rd, a.dy, row * a.lddy, a.cols, t);
+        load_row<HBF, W>(rh, a.h, row * a.ldh, a.cols, t);
+        if (a.dh)
+            load_row<HBF, W>(re, a.dh, row * a.lddh, a.cols, t);
+        float d[CH][8], h[CH][8], e[CH][8];
         float sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < CH; u++) {
-            const int c = 8 * (u * 64 * W + t);
-            if (c < a.cols) {
-                widen<DBF>(load8<DBF>(a.dy, row * a.lddy + c), d[u]);
-                widen<HBF>(load8<HBF>(a.h, row * a.ldh + c), h[u]);
+            widen<DBF>(rd[u], d[u]);
+            widen<HBF>(rh[u], h[u]);
+            if (a.dh)
+                widen<HBF>(re[u], e[u]);
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    h[u][i] *= rstd;
-                    dw[u][i] += d[u][i] * h[u][i];
-                    d[u][i] *= w[u][i];
-                    sum += d[u][i] * h[u][i];
-                }
+            for (int i = 0; i < 8; i++) {
+                h[u][i] *= rstd;
+                dw[u][i] = fmaf(d[u][i], h[u][i], dw[u][i]);
+                d[u][i] *= w[u][i];
+                sum = fmaf(d[u][i], h[u][i], sum);
+                if (!a.dh)
+                    e[u][i] = 0.0f;
             }
         }
         const float mean = row_sum<W>(sum, red[odd]) / (float)a.cols;
         odd ^= 1;
 #pragma unroll
         for (int u = 0; u < CH; u++) {
-            const int c = 8 * (u * 64 * W + t);
+            const int c = chunk_col<W>(u, t);
             if (c < a.cols) {
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    o[i] = rstd * (d[u][i] - h[u][i] * mean);
-                if (a.dh) {
-                    float e[8];
-                    widen<HBF>(load8<HBF>(a.dh, row * a.lddh + c), e);
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        o[i] += e[i];
-                }
+                    o[i] = fmaf(rstd, fmaf(h[u][i], -mean, d[u][i]), e[u][i]);
                 store8<HBF>(a.dx, row * a.lddx + c, narrow<HBF>(o));
             }
         }
     }
 #pragma unroll
     for (int u = 0; u < CH; u++) {
-        const int c = 8 * (u * 64 * W + t);
-        if (c < a.cols && first < a.parts) {
+        const int c = chunk_col<W>(u, t);
+        if (c < a.cols) {
             float *p = a.part + first * a.cols + c;
             *reinterpret_cast<float4 *>(p) = make_float4(dw[u][0], dw[u][1], dw[u][2], dw[u][3]);
             *reinterpret_cast<float4 *>(p + 4) = make_float4(dw[u][4], dw[u][5], dw[u][6], dw[u][7]);
@@ -263,9 +282,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(NormGradArgs a)
 {
     __shared__ float red[32][33];
     const int col = threadIdx.x & 31, slice = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
+    const float *p = a.part + c; // (cols is a multiple of 32)
     float v = 0.0f;
-    for (int p = slice; p < a.parts; p += 32)
-        v += a.part[(int64_t)p * a.cols + c]; // (cols is a multiple of 32)
+    for (int i = slice; i < a.parts; i += 32 * 8) { // eight loads together, the last part again past the end
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            f[k] = p[(int64_t)min(i + 32 * k, a.parts - 1) * a.cols];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            v += i + 32 * k < a.parts ? f[k] : 0.0f;
+    }
     red[slice][col] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -325,7 +352,7 @@ template <bool XBF, bool HBF, bool RES> static void launch_norm(const NormArgs &
     do {                                                                                                               \
         const int64_t n = (a.rows + NORM_ROWS<W> - 1) / NORM_ROWS<W>;                                                  \
         rmsnorm_kernel<XBF, HBF, RES, W, CH>                                                                           \
-            <<<(unsigned)(n < 4096 ? n : 4096), NORM_THREADS<W>, 0, st>>>(a);                                          \
+            <<<(unsigned)(n < 2048 ? n : 2048), NORM_THREADS<W>, 0, st>>>(a);                                          \
     } while (0)
     FGB_NORM_VARIANT(a.cols, FGB_N);
 #undef FGB_N

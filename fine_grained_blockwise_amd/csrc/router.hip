@@ -1,8 +1,113 @@
-// router.hip -- the MoE router's sums over workgroups, its gradient and its entry points
-// (the mathematics and the forward kernel: router_kernel.h).
-#include "router_kernel.h"
+// router.hip -- the MoE router's kernels and entry points (the mathematics and what it shares
+// with the choice by a bias and groups: router_device.h).
+#include "router_device.h"
 
 namespace fgb {
+
+template <bool BF16, int SCORE, int L, int Q>
+__global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
+{
+    extern __shared__ float red[]; // [groups][E] floats (the loss's sums), then E + 1 ints
+    constexpr int GROUPS = 256 / L, R = 4 * Q;
+    const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = 4 * l;
+    int *cnt = reinterpret_cast<int *>(red + (a.loss ? GROUPS * a.E : 0));
+    __shared__ int ids[BF16 ? 1 : 256]; // [groups][L]
+    for (int e = threadIdx.x; e <= a.E; e += 256)
+        cnt[e] = 0;
+    __syncthreads();
+    float psum[R];
+    int live_n = 0;
+#pragma unroll
+    for (int j = 0; j < R; j++)
+        psum[j] = 0.0f;
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t t = t0 + group;
+        const bool on = t < a.T && (!a.mask || a.mask[t] != 0);
+        float z[R];
+        uint32_t key[R], best = 0;
+        load_logits<BF16, L, Q>(a, min(t, a.T - 1), e0, z);
+#pragma unroll
+        for (int j = 0; j < R; j++) {
+            key[j] = on ? logit_key<BF16>(z[j], e0 + at_quad<L>(j)) : 0u;
+            best = max(best, key[j]);
+        }
+        uint32_t top = group_max<L>(best);
+        const uint32_t first = top; // 0: the token is not live
+        // topk rounds; lane r keeps the r-th choice's key (and, through LDS, its id)
+        uint32_t mine = 0;
+        for (int r = 0; r < a.k; r++) {
+            mine = l == r ? top : mine;
+            best = 0;
+            if constexpr (BF16) { // one expert has this key (no expert: all have 0)
+#pragma unroll
+                for (int j = 0; j < R; j++) {
+                    key[j] = key[j] == top ? 0u : key[j];
+                    best = max(best, key[j]);
+                }
+            } else {
+                int at = NOWHERE; // the lane's lowest id with the largest key, less e0
+#pragma unroll
+                for (int j = R - 1; j >= 0; j--)
+                    at = key[j] == top ? at_quad<L>(j) : at;
+                const uint64_t some = __ballot(top != 0), hits = some & __ballot(at != NOWHERE);
+                if constexpr (Q == 1) { // ids grow with the lane: the lowest lane's
+                    const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
+                                            : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
+                                                            (L == 32 ? 0x80000000u : 1u << (L & 31)));
+                    at = l == win ? at : NOWHERE;
+                } else if (__builtin_popcountll(hits) * L > __builtin_popcountll(some)) {
+                    // equal logits in several lanes of a token
+                    const int lowest = ~(int)group_max<L>(at == NOWHERE ? 0u : ~(uint32_t)(e0 + at));
+                    at = e0 + at == lowest ? at : NOWHERE;
+                }
+                if (at != NOWHERE)
+                    ids[group * L + r] = e0 + at;
+#pragma unroll
+                for (int j = 0; j < R; j++) {
+                    key[j] = at == at_quad<L>(j) ? 0u : key[j];
+                    best = max(best, key[j]);
+                }
+            }
+            top = group_max<L>(best);
+        }
+        int mine_e = -1;
+        if constexpr (BF16) {
+            mine_e = mine ? key_expert_bf16(mine) : -1;
+        } else {
+            wave_sync();
+            if (mine)
+                mine_e = ids[threadIdx.x];
+            wave_sync();
+        }
+        if (mine)
+            atomicAdd(&cnt[mine_e], 1); // integers: any order gives the same counts
+        float num[R], p[R];
+        Sig sg[R];
+        const Norm n = probabilities<SCORE, L, R>(z, key_logit<BF16>(first), num, p, sg);
+        // lane r: the weight of slot r
+        const float zr = key_logit<BF16>(mine);
+        const float nr = mine ? numerator<SCORE>(zr, n.m) : 0.0f;
+        float w = nr * n.inv;
+        if (a.renorm) {
+            w = nr / group_sum<L>(nr);
+            // (a NaN logit is not chosen, but must not go unseen either)
+            w = n.inv == n.inv ? w : n.inv;
+        } else if (SCORE == FGB_ROUTER_SIGMOID) {
+            w = sigmoid(zr).s;
+        }
+        if (t < a.T && l < a.k) {
+            a.idx[t * a.k + l] = mine_e;
+            a.w[t * a.k + l] = mine_e < 0 ? 0.0f : a.scale * w;
+        }
+        if (first != 0) {
+            live_n++;
+#pragma unroll
+            for (int j = 0; j < R; j++)
+                psum[j] += p[j];
+        }
+    }
+    finish_workgroup<L, R>(a, red, cnt, psum, live_n);
+}
 
 // Counts and loss from the workgroups' partial results: COLS experts a workgroup, 1024 /
 // COLS threads to an expert, added in a fixed order; the first workgroup takes the live
@@ -110,6 +215,81 @@ template <int COLS> __global__ __launch_bounds__(64 * RED_WAVES) void router_red
         write_loss(a, sum, live);
 }
 
+// Tokens whose chosen experts lie far below the largest logit, as a bias or groups can choose
+// them: beside it their numerators vanish, so a renormed weight's part is formed from the
+// largest chosen logit.  (Where the largest logit is chosen the numerators sum to at least
+// 1/2.)  The pass over the tokens leaves them to this one, which reads the logits again for
+// each step: it is rare, and in the usual pass its registers cost 3% (32768 x 512 forward and
+// backward: 82.5 us, 79.6 without).  It takes tokens up to twice the limit, so that none falls
+// between the two roundings of the sum.
+constexpr float FAR = 0x1p-60f;
+
+template <bool BF16, int SCORE, int L>
+__device__ __forceinline__ void router_bwd_far(const RouterArgs &a, float *part, float f)
+{
+    constexpr int GROUPS = 256 / L;
+    const int l = threadIdx.x % L, group = threadIdx.x / L;
+#pragma unroll 1
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t t = min(t0 + group, a.T - 1);
+        const auto logit = [&](int e) {
+            return BF16 ? __uint_as_float((uint32_t)((const uint16_t *)a.z)[t * a.ldz + e] << 16)
+                        : ((const float *)a.z)[t * a.ldz + e];
+        };
+        const int slot = t0 + group < a.T && l < a.k ? a.idx[t * a.k + l] : -1;
+        const bool on = slot >= 0 && slot < a.E;
+        uint32_t best = 0;
+#pragma unroll 1
+        for (int e = l; e < a.E; e += L)
+            best = max(best, logit_key<false>(logit(e), 0));
+        float m = key_logit<false>(group_max<L>(best));
+        m = SCORE == FGB_ROUTER_SIGMOID ? fminf(m, 0.0f) : m;
+        const float zr = on ? logit(slot) : NEG_INF;
+        const float total = group_sum<L>(on ? numerator<SCORE>(zr, m) : 0.0f);
+        const bool live = group_max<L>(on) != 0, far = live && total < 2.0f * FAR;
+        if (!__any(far))
+            continue;
+        // the slots' parts, to their experts
+        float mc = key_logit<false>(group_max<L>(logit_key<false>(zr, 0)));
+        mc = SCORE == FGB_ROUTER_SIGMOID ? fminf(mc, 0.0f) : mc;
+        const float D = on && a.dw ? a.scale * a.dw[t * a.k + l] : 0.0f;
+        const float n = on ? numerator<SCORE>(zr, mc) : 0.0f;
+        const float share = n / group_sum<L>(n);
+        const float mean = group_sum<L>(on ? D * share : 0.0f);
+        wave_sync();
+#pragma unroll 1
+        for (int e = l; e < a.E; e += L)
+            part[e] = 0.0f;
+        wave_sync();
+        if (on)
+            part[slot] = share * (D - mean);
+        wave_sync();
+        // the loss's part
+        float sum = 0.0f, gp = 0.0f;
+#pragma unroll 1
+        for (int e = l; e < a.E; e += L) {
+            const float v = numerator<SCORE>(logit(e), m);
+            sum += v;
+            gp += f * (float)a.counts[e] * v;
+        }
+        const float inv = 1.0f / group_sum<L>(sum);
+        gp = group_sum<L>(gp) * inv;
+#pragma unroll 1
+        for (int e = l; e < a.E; e += L) {
+            const float z = logit(e), p = numerator<SCORE>(z, m) * inv;
+            float dz = p * (f * (float)a.counts[e] - gp) + part[e];
+            if constexpr (SCORE == FGB_ROUTER_SIGMOID)
+                dz *= sigmoid(z).one_minus;
+            if (far) {
+                if constexpr (BF16)
+                    ((__bf16 *)a.dz)[t * a.lddz + e] = (__bf16)dz;
+                else
+                    ((float *)a.dz)[t * a.lddz + e] = dz;
+            }
+        }
+    }
+}
+
 template <bool BF16, int SCORE, int L, int Q>
 __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
 {
@@ -119,6 +299,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
     const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = 4 * l;
     uint4 *quads = lds + group * (L * Q);
     uint32_t *mine = reinterpret_cast<uint32_t *>(quads);
+    bool any_far = false;
     const int n = a.counts[a.E];
     const float dl = a.dloss ? *a.dloss : 0.0f;
     const float f = n > 0 ? (float)((double)dl * a.coef * a.E / ((double)a.k * n * n)) : 0.0f;
@@ -174,34 +355,13 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
         gp = group_sum<L>(gp);
         dv = group_sum<L>(dv);
         float mean = 0.0f, inv = 1.0f;
+        bool far = false;
         if (a.renorm) {
             const float total = group_sum<L>(chosen);
             inv = 1.0f / total;
             mean = dv * inv;
-            // A bias or groups can choose experts far below the largest logit: their numerators are
-            // formed again from the largest of them.  (Where the largest logit is chosen the sum is
-            // at least 1/2.)
-            const bool far = live && total < 0x1p-60f;
-            if (__any(far)) {
-                best = 0;
-#pragma unroll
-                for (int j = 0; j < R; j++)
-                    best = max(best, on[j] ? logit_key<false>(z[j], 0) : 0u);
-                const float most = key_logit<false>(group_max<L>(best));
-                float sum = 0.0f, dsum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < R; j++) {
-                    const float t = on[j] ? numerator<SCORE>(z[j], SCORE == FGB_ROUTER_SIGMOID ? fminf(most, 0.0f) : most)
-                                          : 0.0f;
-                    v[j] = far ? t : v[j];
-                    sum += t;
-                    dsum += d[j] * t;
-                }
-                sum = group_sum<L>(sum);
-                dsum = group_sum<L>(dsum);
-                inv = far ? 1.0f / sum : inv;
-                mean = far ? dsum * inv : mean;
-            }
+            far = live && total < FAR;
+            any_far |= __any(far) != 0;
         }
 #pragma unroll
         for (int j = 0; j < R; j++) {
@@ -216,7 +376,7 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             }
             dz[j] = !live ? 0.0f : on[j] ? q + w : q;
         }
-        if (t >= a.T)
+        if (t >= a.T || far)
             continue;
         const int64_t row = t * a.lddz;
 #pragma unroll
@@ -241,6 +401,26 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             }
         }
     }
+    if (any_far)
+        router_bwd_far<BF16, SCORE, L>(a, reinterpret_cast<float *>(quads), f);
+}
+
+template <bool BF16, int SCORE> static void launch_router_fwd(const RouterArgs &a, hipStream_t st)
+{
+    const int L = at_least_slots(router_lanes(a.E), a.k), groups = 256 / L;
+    const int Q = (a.E + 4 * L - 1) / (4 * L);
+    const unsigned grid = (unsigned)router_blocks(a.T, a.E);
+    const size_t lds = (size_t)4 * ((a.loss ? groups * a.E : 0) + a.E + 1);
+#define FGB_R(LANES, PER)                                                                                              \
+    if (L == LANES && Q == PER)                                                                                        \
+        router_fwd_kernel<BF16, SCORE, LANES, PER><<<grid, 256, lds, st>>>(a);
+#define FGB_L(LANES) FGB_R(LANES, 1) FGB_R(LANES, 2) FGB_R(LANES, 3) FGB_R(LANES, 4)
+    FGB_L(8)
+    FGB_L(16)
+    FGB_L(32)
+    FGB_L(64)
+#undef FGB_L
+#undef FGB_R
 }
 
 template <bool BF16, int SCORE> static void launch_router_bwd(const RouterArgs &a, hipStream_t st)
@@ -339,9 +519,15 @@ extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64
                                        loss_coef, topk_idx, weights, counts, loss, workspace, ws_bytes);
     if (rc != FGB_OK)
         return rc;
-    dispatch_router_fwd<false>(a, dtype, score, (hipStream_t)stream);
+    const hipStream_t st = (hipStream_t)stream;
+    if (dtype == FGB_BF16)
+        score == FGB_ROUTER_SOFTMAX ? launch_router_fwd<true, FGB_ROUTER_SOFTMAX>(a, st)
+                                    : launch_router_fwd<true, FGB_ROUTER_SIGMOID>(a, st);
+    else
+        score == FGB_ROUTER_SOFTMAX ? launch_router_fwd<false, FGB_ROUTER_SOFTMAX>(a, st)
+                                    : launch_router_fwd<false, FGB_ROUTER_SIGMOID>(a, st);
     FGB_LAUNCHED("router_fwd_kernel");
-    return router_finish(a, (hipStream_t)stream);
+    return router_finish(a, st);
 }
 
 extern "C" int moe_router_backward(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk,

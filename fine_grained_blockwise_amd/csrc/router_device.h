@@ -1,4 +1,4 @@
-// router_kernel.h -- the MoE router: the experts of each token, their weights, the
+// router_device.h -- the MoE router: the experts of each token, their weights, the
 // slots per expert, the balance loss, and the gradient of the logits.
 //
 // For logits z [T, E] and a token t that is live (its mask is set and it has an
@@ -41,8 +41,6 @@ template <int L> constexpr __device__ int at_quad(int j) { return j / 4 * 4 * L 
 
 struct RouterArgs {
     const void *z;
-    const float *bias;           // [E] or NULL
-    int groups, topk_groups, of; // groups of `of` experts
     int64_t T, ldz;
     int E, k;
     const uint8_t *mask;
@@ -244,228 +242,15 @@ __device__ __forceinline__ Norm probabilities(const float (&z)[R], float m, floa
     return n;
 }
 
-// The choice by other values than the logits: with a bias c = s + b, the score rounded to
-// FP32 once and the sum once more (so that any correct implementation compares the same
-// numbers), without one c = z.  A group's value is the sum of its two largest c with a bias,
-// its largest c without; experts outside the topk_groups groups of largest value (equal
-// values: the lowest id) lose their keys.
-template <int L, int Q> struct Choice {
-    static constexpr int R = 4 * Q;
-    float bias[R];
-    int of[R];      // the experts' groups
-    uint32_t *keys; // [E] of the token, then its groups' values and whether they are open
-    uint32_t *values, *open;
-
-    // `lds`: GROUPS * (E + 2 groups) words, where groups > 1.
-    __device__ __forceinline__ void begin(const RouterArgs &a, int e0, uint32_t *lds, int group, int groups)
-    {
-#pragma unroll
-        for (int j = 0; j < R; j++) {
-            const int e = min(e0 + at_quad<L>(j), a.E - 1);
-            bias[j] = a.bias ? a.bias[e] : 0.0f;
-            of[j] = e / a.of;
-        }
-        keys = lds + group * a.E;
-        values = lds + groups * a.E + 2 * group * a.groups;
-        open = values + a.groups;
-    }
-
-    // key: the logits' keys (0: unusable), most: the largest usable logit -> the keys of c.
-    template <int SCORE>
-    __device__ __forceinline__ void choose(const RouterArgs &a, const float (&z)[R], float most, int l, int e0,
-                                           uint32_t (&key)[R])
-    {
-        if (a.bias) { // uniform
-            double s[R], inv = 1.0;
-            if constexpr (SCORE == FGB_ROUTER_SOFTMAX) {
-                double sum = 0.0;
-#pragma unroll
-                for (int j = 0; j < R; j++) { // (equal: an infinite one has the score 1, not NaN)
-                    s[j] = !key[j] ? 0.0 : z[j] == most ? 1.0 : exp((double)z[j] - (double)most);
-                    sum += s[j];
-                }
-#pragma unroll
-                for (int d = 1; d < L; d <<= 1)
-                    sum += __shfl_xor(sum, d);
-                inv = 1.0 / sum;
-            } else {
-#pragma unroll
-                for (int j = 0; j < R; j++)
-                    s[j] = 1.0 / (1.0 + exp(-(double)z[j]));
-            }
-#pragma unroll
-            for (int j = 0; j < R; j++) {
-                const float c = (float)(SCORE == FGB_ROUTER_SOFTMAX ? s[j] * inv : s[j]) + bias[j];
-                key[j] = key[j] ? logit_key<false>(c, 0) : 0u;
-            }
-        }
-        if (a.groups == 1) // uniform
-            return;
-#pragma unroll
-        for (int j = 0; j < R; j++)
-            if (e0 + at_quad<L>(j) < a.E)
-                keys[e0 + at_quad<L>(j)] = key[j];
-        wave_sync();
-        for (int g = l; g < a.groups; g += L) {
-            uint32_t first = 0, second = 0;
-            for (int i = 0; i < a.of; i++) {
-                const uint32_t k = keys[g * a.of + i];
-                second = max(second, min(first, k));
-                first = max(first, k);
-            }
-            if (a.bias && second) // (both > 0, so neither is -inf or NaN)
-                first = logit_key<false>(key_logit<false>(first) + key_logit<false>(second), 0);
-            values[g] = first;
-        }
-        wave_sync();
-        for (int g = l; g < a.groups; g += L) {
-            const uint32_t own = values[g];
-            int before = 0;
-            for (int h = 0; h < a.groups; h++) {
-                const uint32_t v = values[h];
-                before += v > own || (v == own && h < g);
-            }
-            open[g] = before < a.topk_groups;
-        }
-        wave_sync();
-#pragma unroll
-        for (int j = 0; j < R; j++)
-            key[j] = open[of[j]] ? key[j] : 0u;
-        wave_sync();
-    }
-};
-
-template <bool BF16, int SCORE, int L, int Q, bool CHOICE>
-__global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
+// The end of a forward workgroup: its counts and sums over tokens (a group's psum and live
+// tokens), groups in order; a lone workgroup finishes.  red: [groups][E], where the loss is
+// wanted; cnt: [E + 1], the choices so far.
+template <int L, int R>
+__device__ __forceinline__ void finish_workgroup(const RouterArgs &a, float *red, int *cnt, const float (&psum)[R],
+                                                 int live_n)
 {
-    extern __shared__ float red[]; // [groups][E] floats (the loss's sums), then E + 1 ints; CHOICE: choose()'s
-    constexpr int GROUPS = 256 / L, R = 4 * Q;
-    constexpr bool NAMED = BF16 && !CHOICE; // a key names its expert
+    constexpr int GROUPS = 256 / L;
     const int l = threadIdx.x % L, group = threadIdx.x / L, e0 = 4 * l;
-    int *cnt = reinterpret_cast<int *>(red + (a.loss ? GROUPS * a.E : 0));
-    __shared__ int ids[NAMED ? 1 : 256];      // [groups][L]
-    __shared__ float chosen[CHOICE ? 256 : 1]; // their logits
-    Choice<L, Q> how;
-    if constexpr (CHOICE)
-        how.begin(a, e0, reinterpret_cast<uint32_t *>(cnt + a.E + 1), group, GROUPS);
-    for (int e = threadIdx.x; e <= a.E; e += 256)
-        cnt[e] = 0;
-    __syncthreads();
-    float psum[R];
-    int live_n = 0;
-#pragma unroll
-    for (int j = 0; j < R; j++)
-        psum[j] = 0.0f;
-    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
-        const int64_t t = t0 + group;
-        const bool on = t < a.T && (!a.mask || a.mask[t] != 0);
-        float z[R];
-        uint32_t key[R], best = 0;
-        load_logits<BF16, L, Q>(a, min(t, a.T - 1), e0, z);
-#pragma unroll
-        for (int j = 0; j < R; j++) {
-            key[j] = on ? logit_key<NAMED>(z[j], e0 + at_quad<L>(j)) : 0u;
-            best = max(best, key[j]);
-        }
-        float most = NEG_INF; // the token's largest logit
-        if constexpr (CHOICE) {
-            most = key_logit<false>(group_max<L>(best));
-            how.template choose<SCORE>(a, z, most, l, e0, key);
-            best = 0;
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                best = max(best, key[j]);
-        }
-        uint32_t top = group_max<L>(best);
-        const uint32_t first = top; // 0: the token is not live
-        // topk rounds; lane r keeps the r-th choice's key (and, through LDS, its id)
-        uint32_t mine = 0;
-        for (int r = 0; r < a.k; r++) {
-            mine = l == r ? top : mine;
-            best = 0;
-            if constexpr (NAMED) { // one expert has this key (no expert: all have 0)
-#pragma unroll
-                for (int j = 0; j < R; j++) {
-                    key[j] = key[j] == top ? 0u : key[j];
-                    best = max(best, key[j]);
-                }
-            } else {
-                int at = NOWHERE; // the lane's lowest id with the largest key, less e0
-#pragma unroll
-                for (int j = R - 1; j >= 0; j--)
-                    at = key[j] == top ? at_quad<L>(j) : at;
-                const uint64_t some = __ballot(top != 0), hits = some & __ballot(at != NOWHERE);
-                if constexpr (Q == 1) { // ids grow with the lane: the lowest lane's
-                    const int win = L == 64 ? __builtin_ctzll(hits | (1ull << 63))
-                                            : __builtin_ctz((uint32_t)(hits >> ((threadIdx.x & 63) & ~(L - 1))) |
-                                                            (L == 32 ? 0x80000000u : 1u << (L & 31)));
-                    at = l == win ? at : NOWHERE;
-                } else if (__builtin_popcountll(hits) * L > __builtin_popcountll(some)) {
-                    // equal logits in several lanes of a token
-                    const int lowest = ~(int)group_max<L>(at == NOWHERE ? 0u : ~(uint32_t)(e0 + at));
-                    at = e0 + at == lowest ? at : NOWHERE;
-                }
-                if (at != NOWHERE) {
-                    ids[group * L + r] = e0 + at;
-                    if constexpr (CHOICE) {
-                        float zr = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < R; j++)
-                            zr = at == at_quad<L>(j) ? z[j] : zr;
-                        chosen[group * L + r] = zr;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < R; j++) {
-                    key[j] = at == at_quad<L>(j) ? 0u : key[j];
-                    best = max(best, key[j]);
-                }
-            }
-            top = group_max<L>(best);
-        }
-        int mine_e = -1;
-        float zr = key_logit<NAMED>(mine);
-        if constexpr (NAMED) {
-            mine_e = mine ? key_expert_bf16(mine) : -1;
-        } else {
-            wave_sync();
-            if (mine) {
-                mine_e = ids[threadIdx.x];
-                if constexpr (CHOICE)
-                    zr = chosen[threadIdx.x];
-            }
-            wave_sync();
-        }
-        if (mine)
-            atomicAdd(&cnt[mine_e], 1); // integers: any order gives the same counts
-        float num[R], p[R];
-        Sig sg[R];
-        const Norm n = probabilities<SCORE, L, R>(z, CHOICE ? most : key_logit<NAMED>(first), num, p, sg);
-        // lane r: the weight of slot r
-        float nr = mine ? numerator<SCORE>(zr, n.m) : 0.0f;
-        float w = nr * n.inv;
-        if (a.renorm) {
-            if constexpr (CHOICE) { // the largest logit need not be among the chosen
-                const float m = key_logit<false>(group_max<L>(mine ? logit_key<false>(zr, 0) : 0u));
-                nr = mine ? numerator<SCORE>(zr, SCORE == FGB_ROUTER_SIGMOID ? fminf(m, 0.0f) : m) : 0.0f;
-            }
-            w = nr / group_sum<L>(nr);
-            // (a NaN logit is not chosen, but must not go unseen either)
-            w = n.inv == n.inv ? w : n.inv;
-        } else if (SCORE == FGB_ROUTER_SIGMOID) {
-            w = sigmoid(zr).s;
-        }
-        if (t < a.T && l < a.k) {
-            a.idx[t * a.k + l] = mine_e;
-            a.w[t * a.k + l] = mine_e < 0 ? 0.0f : a.scale * w;
-        }
-        if (first != 0) {
-            live_n++;
-#pragma unroll
-            for (int j = 0; j < R; j++)
-                psum[j] += p[j];
-        }
-    }
     if (l == 0)
         atomicAdd(&cnt[a.E], live_n);
     if (a.loss) {
@@ -475,7 +260,6 @@ __global__ __launch_bounds__(256) void router_fwd_kernel(RouterArgs a)
                 red[group * a.E + e0 + at_quad<L>(j)] = psum[j];
     }
     __syncthreads();
-    // the workgroup's counts and sums, groups in order; a lone workgroup finishes
     const bool lone = gridDim.x == 1;
     if (!lone && a.loss && blockIdx.x == 0 && threadIdx.x == 0)
         *a.ticket = 0;
@@ -529,36 +313,6 @@ static int64_t router_blocks(int64_t T, int E)
 }
 
 static int reduce_blocks(int E) { return E <= 32 ? 1 : (E + 15) / 16; }
-
-template <bool BF16, int SCORE, bool CHOICE> static void launch_router_fwd(const RouterArgs &a, hipStream_t st)
-{
-    const int L = at_least_slots(router_lanes(a.E), a.k), groups = 256 / L;
-    const int Q = (a.E + 4 * L - 1) / (4 * L);
-    const unsigned grid = (unsigned)router_blocks(a.T, a.E);
-    const size_t words = (size_t)(a.loss ? groups * a.E : 0) + a.E + 1 +
-                         (CHOICE && a.groups > 1 ? (size_t)groups * (a.E + 2 * a.groups) : 0);
-#define FGB_R(LANES, PER)                                                                                              \
-    if (L == LANES && Q == PER)                                                                                        \
-        router_fwd_kernel<BF16, SCORE, LANES, PER, CHOICE><<<grid, 256, 4 * words, st>>>(a);
-#define FGB_L(LANES) FGB_R(LANES, 1) FGB_R(LANES, 2) FGB_R(LANES, 3) FGB_R(LANES, 4)
-    FGB_L(8)
-    FGB_L(16)
-    FGB_L(32)
-    FGB_L(64)
-#undef FGB_L
-#undef FGB_R
-}
-
-// The forward pass by the arguments' types.
-template <bool CHOICE> static void dispatch_router_fwd(const RouterArgs &a, int dtype, int score, hipStream_t st)
-{
-    if (dtype == FGB_BF16)
-        score == FGB_ROUTER_SOFTMAX ? launch_router_fwd<true, FGB_ROUTER_SOFTMAX, CHOICE>(a, st)
-                                    : launch_router_fwd<true, FGB_ROUTER_SIGMOID, CHOICE>(a, st);
-    else
-        score == FGB_ROUTER_SOFTMAX ? launch_router_fwd<false, FGB_ROUTER_SOFTMAX, CHOICE>(a, st)
-                                    : launch_router_fwd<false, FGB_ROUTER_SIGMOID, CHOICE>(a, st);
-}
 
 // What both entry points of the forward pass check, and their arguments (router.hip).
 int check_router(const char *name, const void *z, int dtype, int64_t T, int E, int64_t ldz, int k, int score);

@@ -5,7 +5,8 @@ only marshals arguments: it checks shapes, allocates outputs with
 ``torch.empty`` on the input's device and calls the C entry point of the same
 name on torch's current HIP stream.  All arithmetic runs in the HIP kernels.
 
-There is no fallback: if libfgb.so is missing, importing this package raises.
+There is no fallback: if libfgb.so (or _tensors.so, which looks through lists
+of tensors) is missing, importing this package raises.
 """
 import ctypes as C
 import os
@@ -67,6 +68,8 @@ class FgbError(RuntimeError):
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libfgb.so not found at {LIB_PATH}; build it with "
                       "`python -c 'import __graft_entry__ as g; g.build()'`")
+
+from . import _tensors  # noqa: E402  (needs torch's libraries, loaded above)
 
 _lib = C.CDLL(LIB_PATH)
 _p, _i64, _i32, _sz, _f32, _f64 = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float, C.c_double
@@ -155,10 +158,13 @@ def _call(name, *args):
         raise FgbError(name, rc, _lib.fgb_last_error().decode())
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call_on(dev, name, *args):
     """_call with `dev` as the current device: a launch goes to the current one, and the stream's handle does not
     tell (every device's default stream is 0)."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         _call(name, *args)
     else:
         with torch.cuda.device(dev):
@@ -1116,10 +1122,11 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
         _need(workspace, f"{name}: workspace", dtype=torch.uint8, contiguous=True)
     if bias is not None:
         _need(bias, f"{name}: bias", shape=(E,), dtype=torch.float32, contiguous=True)
-    if not 1 <= groups <= 64 or E % groups:
-        raise ValueError(f"{name}: groups must be in [1, 64] and divide E ({E}), got {groups}")
-    if not 1 <= topk_groups <= groups or topk > topk_groups * (E // groups):
-        raise ValueError(f"{name}: topk_groups must be in [1, groups] and hold topk experts, got {topk_groups}")
+    if groups != 1 or topk_groups != 1:
+        if not 1 <= groups <= 64 or E % groups:
+            raise ValueError(f"{name}: groups must be in [1, 64] and divide E ({E}), got {groups}")
+        if not 1 <= topk_groups <= groups or topk > topk_groups * (E // groups):
+            raise ValueError(f"{name}: topk_groups must be in [1, groups] and hold topk experts, got {topk_groups}")
     dev = _check_dev(logits, token_mask, workspace, bias)
     if workspace is None:
         need = _lib.moe_router_workspace_size(T, E)
@@ -1181,19 +1188,26 @@ def moe_bias_update(bias, counts, rate, out=None):
 
 
 # ---------------------------------------------------------------------------
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 def _norm_rows(t, name, shape=None):
-    """t and its row stride, copied where rows are not 16-byte aligned runs."""
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
+    """t, its type and its row stride; t is copied where its rows are not 16-byte aligned runs."""
+    if len(t.shape) != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be 2-D" if shape is None else f"{name} must have shape {tuple(shape)}, got "
                          f"{tuple(t.shape)}")
-    _dtype_code(t)
+    code = _CODES.get(t.dtype)
+    if code is None:
+        _dtype_code(t)
     if not t.is_cuda:
         raise ValueError("all tensors must be on the GPU")
     rows, cols = t.shape
+    if t.data_ptr() % 16 == 0 and t.is_contiguous():  # (rows are whole 16-byte runs: cols % 32 == 0)
+        return t, code, cols
     ld = t.stride(0) if rows > 1 else cols
     if (cols > 1 and t.stride(1) != 1) or ld < cols or ld * t.element_size() % 16 or t.data_ptr() % 16:
-        return t.clone(memory_format=torch.contiguous_format), cols
-    return t, ld
+        return t.clone(memory_format=torch.contiguous_format), code, cols
+    return t, code, ld
 
 
 def _norm_out(t, name, shape, dtype):
@@ -1207,11 +1221,15 @@ def _norm_out(t, name, shape, dtype):
 
 
 def _norm_weight(weight, cols, name):
-    _need(weight, f"{name}: weight", shape=(cols,))
-    _dtype_code(weight)
+    """The weight and its type; it is copied where it is no 16-byte aligned run."""
+    if weight.shape != (cols,):
+        _need(weight, f"{name}: weight", shape=(cols,))
+    code = _CODES.get(weight.dtype)
+    if code is None:
+        _dtype_code(weight)
     if not weight.is_contiguous() or weight.data_ptr() % 16:
         weight = weight.clone(memory_format=torch.contiguous_format)
-    return weight
+    return weight, code
 
 
 def _norm_cols(cols, name):
@@ -1235,17 +1253,18 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
         raise ValueError(f"{name}: eps must be positive")
     if h is not None and residual is None:
         raise ValueError(f"{name}: h needs a residual")
-    x, ldx = _norm_rows(x, f"{name}: x")
-    rows, cols = x.shape
+    x, x_code, ldx = _norm_rows(x, "rmsnorm_quant: x")
+    rows, cols = shape = x.shape
     _norm_cols(cols, name)
     if quant and cols % group:
         raise ValueError(f"{name}: cols ({cols}) must be a multiple of the group ({group})")
-    weight = _norm_weight(weight, cols, name)
-    ldr = ldh = ldy = cols
+    weight, w_code = _norm_weight(weight, cols, name)
+    ldr = ldh = cols
+    r_code = F32
     if residual is not None:
-        residual, ldr = _norm_rows(residual, f"{name}: residual", x.shape)
+        residual, r_code, ldr = _norm_rows(residual, "rmsnorm_quant: residual", shape)
         if h is not None:
-            ldh = _norm_out(h, f"{name}: h", x.shape, residual.dtype)
+            ldh = _norm_out(h, f"{name}: h", shape, residual.dtype)
     dev = _check_dev(x, weight, residual, h)
     if residual is not None and h is None:
         h = torch.empty(rows, cols, dtype=residual.dtype, device=dev)
@@ -1256,10 +1275,9 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
         q = torch.empty(rows, cols, dtype=_U8, device=dev)
         s = torch.empty(rows, cols // group, dtype=_U8, device=dev)
     rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    _call_on(dev, name, x.data_ptr(), _dtype_code(x), rows, cols, ldx, _ptr(residual),
-             F32 if residual is None else _dtype_code(residual), ldr, weight.data_ptr(), _dtype_code(weight), eps, group,
-             _ptr(h), ldh, rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _dtype_code(y), ldy,
-             _stream(x))
+    _call_on(dev, name, x.data_ptr(), x_code, rows, cols, ldx, _ptr(residual), r_code, ldr, weight.data_ptr(), w_code,
+             eps, group, _ptr(h), ldh, rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype],
+             cols, _stream(x))
     return q, s, y, x if h is None else h, rstd
 
 
@@ -1274,18 +1292,18 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
     dx is the gradient of h, and so of x and the residual, with dh (what reaches h past the norm, in h's dtype) added
     before its rounding; dx= takes a tensor for it, which may be dh or dy itself."""
     name = "rmsnorm_backward"
-    dy, lddy = _norm_rows(dy, f"{name}: dy")
-    rows, cols = dy.shape
+    dy, dy_code, lddy = _norm_rows(dy, "rmsnorm_backward: dy")
+    rows, cols = shape = dy.shape
     _norm_cols(cols, name)
-    h, ldh = _norm_rows(h, f"{name}: h", dy.shape)
-    weight = _norm_weight(weight, cols, name)
+    h, h_code, ldh = _norm_rows(h, "rmsnorm_backward: h", shape)
+    weight, w_code = _norm_weight(weight, cols, name)
     _need(rstd, f"{name}: rstd", shape=(rows,), dtype=torch.float32, contiguous=True)
     lddh = lddx = cols
     if dh is not None:
-        _need(dh, f"{name}: dh", dtype=h.dtype)
-        dh, lddh = _norm_rows(dh, f"{name}: dh", dy.shape)
+        _need(dh, "rmsnorm_backward: dh", dtype=h.dtype)
+        dh, _, lddh = _norm_rows(dh, "rmsnorm_backward: dh", shape)
     if dx is not None:
-        lddx = _norm_out(dx, f"{name}: dx", dy.shape, h.dtype)
+        lddx = _norm_out(dx, f"{name}: dx", shape, h.dtype)
     if workspace is not None:
         _need(workspace, f"{name}: workspace", dtype=_U8, contiguous=True)
     dev = _check_dev(dy, h, weight, rstd, dh, dx, workspace)
@@ -1294,30 +1312,22 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
     if workspace is None:
         workspace = torch.empty(_lib.rmsnorm_backward_workspace_size(rows, cols), dtype=_U8, device=dev)
     dweight = torch.empty(cols, dtype=torch.float32, device=dev)
-    _call_on(dev, name, dy.data_ptr(), _dtype_code(dy), rows, cols, lddy, h.data_ptr(), _dtype_code(h), ldh,
-             weight.data_ptr(), _dtype_code(weight), rstd.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), lddx,
+    _call_on(dev, name, dy.data_ptr(), dy_code, rows, cols, lddy, h.data_ptr(), h_code, ldh,
+             weight.data_ptr(), w_code, rstd.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), lddx,
              dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dy))
     return dx, dweight
 
 
 # ---------------------------------------------------------------------------
-def _grad_list(grads, name, what="gradient"):
-    """Checks of a list of gradients: (n, pointers, lengths, type codes, device)."""
-    dev = None
-    for i, g in enumerate(grads):
-        if not g.is_cuda:
-            raise ValueError("all tensors must be on the GPU")
-        if dev is None:
-            dev = g.device
-        elif g.device != dev:
-            raise ValueError("all tensors must be on the same GPU")
-        if not g.is_contiguous():
-            raise ValueError(f"{name}: {what} {i} must be contiguous")
-    if dev is None:
+def _grad_list(grads, name):
+    """Checks of a list of gradients: (n, addresses, lengths, types, device), the arrays as bytes objects."""
+    try:
+        at, lengths, types, _ = _tensors.describe(grads)
+    except (TypeError, ValueError) as e:
+        raise type(e)(f"{name}: {e}") from None
+    if not types:
         raise ValueError(f"{name}: the list is empty")
-    n = len(grads)
-    return (n, (C.c_void_p * n)(*[g.data_ptr() for g in grads]), (C.c_int64 * n)(*[g.numel() for g in grads]),
-            (C.c_int * n)(*[_dtype_code(g) for g in grads]), dev)
+    return len(grads), at, lengths, types, grads[0].device
 
 
 def grad_sumsq_workspace_size(numel):
@@ -1373,12 +1383,12 @@ def grad_clip(grads, max_norm, scale=1.0, out=None, sumsq=None, workspace=None):
         out = list(out)
         if len(out) != n:
             raise ValueError(f"{name}: out must hold {n} tensors, got {len(out)}")
-        _, optrs, olen, otypes, odev = _grad_list(out, name, "output")
+        _, optrs, olen, otypes, odev = _grad_list(out, f"{name}: out")
         if odev != dev:
             raise ValueError("all tensors must be on the same GPU")
-        for i in range(n):
-            if olen[i] != numel[i]:
-                raise ValueError(f"{name}: output {i} must hold {numel[i]} elements, got {olen[i]}")
+        if olen != numel:
+            i = [a.numel() != b.numel() for a, b in zip(out, grads)].index(True)
+            raise ValueError(f"{name}: output {i} must hold {grads[i].numel()} elements, got {out[i].numel()}")
     if sumsq is not None:
         _grad_scalar(sumsq, f"{name}: sumsq", dev)
     else:

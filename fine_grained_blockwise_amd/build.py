@@ -3,17 +3,21 @@
 Every .hip file under csrc/ is compiled with hipcc to an object, then linked
 into fine_grained_blockwise_amd/libfgb.so.  Packed-FP32 VALU ops are disabled
 and floating-point contraction is off, so every fp32 operation rounds where
-the source says it does.
+the source says it does.  Beside it _tensors.so, the binding's helper for lists
+of tensors, is compiled against the installed torch (host code only).
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfgb.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -38,12 +42,27 @@ def _compile(src):
     return obj, r.stderr
 
 
+def _build_tensors():
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = TENSORS + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", os.path.join(torch, "include"),
+           "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_list.cpp"),
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for tensor_list.cpp:\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+
+
 def build(jobs=8, verbose=False):
-    """Compile every HIP source and link libfgb.so; returns the library path."""
+    """Compile every HIP source and link libfgb.so, and _tensors.so; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(jobs, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(jobs, len(srcs) + 1)) as ex:
+        tensors = ex.submit(_build_tensors)
         results = list(ex.map(_compile, srcs))
+        tensors.result()
     if verbose:
         for obj, err in results:
             if err.strip():

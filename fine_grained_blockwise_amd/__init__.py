@@ -1128,13 +1128,13 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
         if not 1 <= topk_groups <= groups or topk > topk_groups * (E // groups):
             raise ValueError(f"{name}: topk_groups must be in [1, groups] and hold topk experts, got {topk_groups}")
     dev = _check_dev(logits, token_mask, workspace, bias)
-    if workspace is None:
-        need = _lib.moe_router_workspace_size(T, E)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    idx = torch.empty(T, topk, dtype=torch.int32, device=dev)
-    weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
-    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev) if loss_coef else None
+    need = 0 if workspace is not None else _lib.moe_router_workspace_size(T, E)
+    idx, weights, counts, *more = _tensors.empties(
+        logits, (_KI32, T, topk), (F32, T, topk), (_KI32, E + 1), *(((_KU8, need),) if need else ()),
+        *(((F32,),) if loss_coef else ()))
+    if need:
+        workspace = more[0]
+    loss = more[-1] if loss_coef else None
     out = (score, int(bool(renorm)), scale, loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss),
            _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(logits))
     if bias is None and groups == 1:
@@ -1163,7 +1163,7 @@ def moe_router_backward(logits, topk_idx, counts, dweights=None, dloss=None, sco
         if dloss.numel() != 1:
             raise ValueError(f"{name}: dloss must hold one value")
     _check_dev(logits, topk_idx, counts, dweights, dloss)
-    dz = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    dz, = _tensors.empties(logits, (dt, T, E))
     _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(topk_idx), _ptr(counts), _ptr(dweights),
           _ptr(dloss), score, int(bool(renorm)), scale, loss_coef, _ptr(dz), E, _stream(logits))
     return dz
@@ -1182,13 +1182,14 @@ def moe_bias_update(bias, counts, rate, out=None):
         _need(out, f"{name}: out", shape=(E,), dtype=torch.float32, contiguous=True)
     dev = _check_dev(bias, counts, out)
     if out is None:
-        out = torch.empty_like(bias)
+        out, = _tensors.empties(bias, (F32, E))
     _call_on(dev, name, bias.data_ptr(), counts.data_ptr(), E, rate, out.data_ptr(), _stream(bias))
     return out
 
 
 # ---------------------------------------------------------------------------
-_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}  # (also _tensors.empties' kinds, with the two below)
+_KU8, _KI32 = 2, 3
 
 
 def _norm_rows(t, name, shape=None):
@@ -1266,15 +1267,19 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
         if h is not None:
             ldh = _norm_out(h, f"{name}: h", shape, residual.dtype)
     dev = _check_dev(x, weight, residual, h)
-    if residual is not None and h is None:
-        h = torch.empty(rows, cols, dtype=residual.dtype, device=dev)
-    y = q = s = None
-    if y_dtype is not None:
-        y = torch.empty(rows, cols, dtype=_out_dtype(y_dtype, name), device=dev)
-    if quant:
-        q = torch.empty(rows, cols, dtype=_U8, device=dev)
-        s = torch.empty(rows, cols // group, dtype=_U8, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    if quant and y_dtype is None and h is None and residual is not None:  # the usual outputs in one call
+        y = None
+        h, q, s, rstd = _tensors.empties(x, (r_code, rows, cols), (_KU8, rows, cols), (_KU8, rows, cols // group),
+                                         (F32, rows))
+    else:
+        y = q = s = None
+        rstd, = _tensors.empties(x, (F32, rows))
+        if residual is not None and h is None:
+            h, = _tensors.empties(x, (r_code, rows, cols))
+        if y_dtype is not None:
+            y, = _tensors.empties(x, (_CODES[_out_dtype(y_dtype, name)], rows, cols))
+        if quant:
+            q, s = _tensors.empties(x, (_KU8, rows, cols), (_KU8, rows, cols // group))
     _call_on(dev, name, x.data_ptr(), x_code, rows, cols, ldx, _ptr(residual), r_code, ldr, weight.data_ptr(), w_code,
              eps, group, _ptr(h), ldh, rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype],
              cols, _stream(x))
@@ -1307,11 +1312,15 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
     if workspace is not None:
         _need(workspace, f"{name}: workspace", dtype=_U8, contiguous=True)
     dev = _check_dev(dy, h, weight, rstd, dh, dx, workspace)
-    if dx is None:
-        dx = torch.empty(rows, cols, dtype=h.dtype, device=dev)
-    if workspace is None:
-        workspace = torch.empty(_lib.rmsnorm_backward_workspace_size(rows, cols), dtype=_U8, device=dev)
-    dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    need = (_KU8, _lib.rmsnorm_backward_workspace_size(rows, cols))
+    if dx is None and workspace is None:
+        dx, workspace, dweight = _tensors.empties(dy, (h_code, rows, cols), need, (F32, cols))
+    else:
+        dweight, = _tensors.empties(dy, (F32, cols))
+        if dx is None:
+            dx, = _tensors.empties(dy, (h_code, rows, cols))
+        if workspace is None:
+            workspace, = _tensors.empties(dy, need)
     _call_on(dev, name, dy.data_ptr(), dy_code, rows, cols, lddy, h.data_ptr(), h_code, ldh,
              weight.data_ptr(), w_code, rstd.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), lddx,
              dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dy))

@@ -409,7 +409,7 @@ template <bool BF16, int SCORE> static void launch_router_fwd(const RouterArgs &
 {
     const int L = at_least_slots(router_lanes(a.E), a.k), groups = 256 / L;
     const int Q = (a.E + 4 * L - 1) / (4 * L);
-    const unsigned grid = (unsigned)router_blocks(a.T, a.E);
+    const unsigned grid = (unsigned)router_blocks(a.T, router_lanes(a.E));
     const size_t lds = (size_t)4 * ((a.loss ? groups * a.E : 0) + a.E + 1);
 #define FGB_R(LANES, PER)                                                                                              \
     if (L == LANES && Q == PER)                                                                                        \
@@ -455,7 +455,7 @@ int check_router(const char *name, const void *z, int dtype, int64_t T, int E, i
     return FGB_OK;
 }
 
-int router_forward_args(const char *name, RouterArgs &a, const void *logits, int dtype, int64_t T, int E, int64_t ld,
+int router_forward_args(const char *name, RouterArgs &a, int64_t blocks, const void *logits, int dtype, int64_t T, int E, int64_t ld,
                         int topk, const uint8_t *token_mask, int score, int renorm, float scale, float loss_coef,
                         int32_t *topk_idx, float *weights, int32_t *counts, float *loss, void *workspace,
                         size_t ws_bytes)
@@ -470,7 +470,6 @@ int router_forward_args(const char *name, RouterArgs &a, const void *logits, int
     FGB_REQUIRE(need == 0 || (workspace && ws_bytes >= need), FGB_EWORKSPACE, "%s: workspace of %zu bytes needed", name,
                 need);
     FGB_REQUIRE(((uintptr_t)workspace & 7) == 0, FGB_EINVAL, "%s: workspace must be 8-byte aligned", name);
-    const int64_t blocks = router_blocks(T, E);
     a.z = logits; a.T = T; a.ldz = ld; a.E = E; a.k = topk; a.mask = token_mask;
     a.renorm = renorm; a.scale = scale; a.coef = loss_coef;
     a.idx = topk_idx; a.w = weights; a.counts = counts; a.loss = loss;
@@ -483,15 +482,15 @@ int router_forward_args(const char *name, RouterArgs &a, const void *logits, int
     return FGB_OK;
 }
 
-int router_finish(const RouterArgs &a, hipStream_t st)
+int router_finish(const RouterArgs &a, int64_t blocks, hipStream_t st)
 {
-    const int blocks = (int)router_blocks(a.T, a.E), n = reduce_blocks(a.E);
+    const int n = reduce_blocks(a.E);
     if (blocks == 1)
         return FGB_OK;
     if (n == 1)
-        router_reduce_kernel<32><<<n, 64 * RED_WAVES, 0, st>>>(a, blocks);
+        router_reduce_kernel<32><<<n, 64 * RED_WAVES, 0, st>>>(a, (int)blocks);
     else
-        router_reduce_kernel<16><<<n, 64 * RED_WAVES, 0, st>>>(a, blocks);
+        router_reduce_kernel<16><<<n, 64 * RED_WAVES, 0, st>>>(a, (int)blocks);
     FGB_LAUNCHED("router_reduce_kernel");
     return FGB_OK;
 }
@@ -504,7 +503,8 @@ extern "C" size_t moe_router_workspace_size(int64_t T, int E)
 {
     if (T < 0 || E < 1 || E > 1024)
         return 0;
-    const int64_t blocks = router_blocks(T, E);
+    const int64_t plain = router_blocks(T, router_lanes(E)), grouped = router_blocks(T, grouped_lanes(T, E));
+    const int64_t blocks = plain > grouped ? plain : grouped;
     return blocks == 1 ? 0 : (size_t)(reduce_blocks(E) + 1) * 8 + (size_t)blocks * (2 * (size_t)E + 1) * 4;
 }
 
@@ -515,7 +515,8 @@ extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64
 {
     clear_error();
     RouterArgs a{};
-    const int rc = router_forward_args("moe_router", a, logits, dtype, T, E, ld, topk, token_mask, score, renorm, scale,
+    const int64_t blocks = router_blocks(T, router_lanes(E));
+    const int rc = router_forward_args("moe_router", a, blocks, logits, dtype, T, E, ld, topk, token_mask, score, renorm, scale,
                                        loss_coef, topk_idx, weights, counts, loss, workspace, ws_bytes);
     if (rc != FGB_OK)
         return rc;
@@ -527,7 +528,7 @@ extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64
         score == FGB_ROUTER_SOFTMAX ? launch_router_fwd<false, FGB_ROUTER_SOFTMAX>(a, st)
                                     : launch_router_fwd<false, FGB_ROUTER_SIGMOID>(a, st);
     FGB_LAUNCHED("router_fwd_kernel");
-    return router_finish(a, st);
+    return router_finish(a, blocks, st);
 }
 
 extern "C" int moe_router_backward(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk,

@@ -306,21 +306,33 @@ static int at_least_slots(int L, int k)
 
 // Workgroups of the forward pass, at most three per CU (four: 16384 x 256 24 against
 // 22 us, more partial results to add); one alone needs no second launch.
-static int64_t router_blocks(int64_t T, int E)
+static int64_t router_blocks(int64_t T, int L)
 {
-    const int64_t per = 256 / router_lanes(E), n = (T + per - 1) / per;
+    const int64_t per = 256 / L, n = (T + per - 1) / per;
     return n < 1 ? 1 : n < 768 ? n : 768;
+}
+// Lanes per token where a bias or groups choose.
+#ifndef TL64
+#define TL64 4
+#endif
+#ifndef TL32
+#define TL32 0
+#endif
+static int grouped_lanes(int64_t T, int E)
+{
+    const int L = router_lanes(E);
+    return T <= TL64 ? 64 : T <= TL32 && L < 32 ? 32 : L;
 }
 
 static int reduce_blocks(int E) { return E <= 32 ? 1 : (E + 15) / 16; }
 
 // What both entry points of the forward pass check, and their arguments (router.hip).
 int check_router(const char *name, const void *z, int dtype, int64_t T, int E, int64_t ldz, int k, int score);
-int router_forward_args(const char *name, RouterArgs &a, const void *logits, int dtype, int64_t T, int E, int64_t ld,
+int router_forward_args(const char *name, RouterArgs &a, int64_t blocks, const void *logits, int dtype, int64_t T, int E, int64_t ld,
                         int topk, const uint8_t *token_mask, int score, int renorm, float scale, float loss_coef,
                         int32_t *topk_idx, float *weights, int32_t *counts, float *loss, void *workspace,
                         size_t ws_bytes);
 // Adds the workgroups' partial results, where there are several.
-int router_finish(const RouterArgs &a, hipStream_t st);
+int router_finish(const RouterArgs &a, int64_t blocks, hipStream_t st);
 
 } // namespace fgb

@@ -338,10 +338,9 @@ __global__ __launch_bounds__(256) void router_grouped_kernel(GroupedArgs a)
 
 template <bool BF16, int SCORE> static void launch_grouped(GroupedArgs a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)router_blocks(a.T, a.E);
-    // A few tokens wait for the longest one: a wave takes each, whatever the experts (1 x 256:
-    // 6.9 us, with 16 lanes 14.6).
-    const int L = at_least_slots(a.T <= 4 ? 64 : router_lanes(a.E), a.k), groups = 256 / L;
+    const int lanes = grouped_lanes(a.T, a.E);
+    const unsigned grid = (unsigned)router_blocks(a.T, lanes);
+    const int L = at_least_slots(lanes, a.k), groups = 256 / L;
     const int Q = (a.E + 4 * L - 1) / (4 * L);
     a.lanes = group_lanes(a.E, a.groups, L);
     const size_t lds = 4 * ((a.loss ? groups * a.E : 0) + a.E + 1 + group_words(a.E, a.groups, L, a.lanes));
@@ -395,7 +394,8 @@ extern "C" int moe_router_grouped(const void *logits, int dtype, int64_t T, int 
                 topk_groups, topk);
     FGB_REQUIRE(((uintptr_t)bias & 3) == 0, FGB_EINVAL, "%s: bias must be 4-byte aligned", name);
     GroupedArgs a{};
-    const int rc = router_forward_args(name, a, logits, dtype, T, E, ld, topk, token_mask, score, renorm, scale, loss_coef,
+    const int64_t blocks = router_blocks(T, grouped_lanes(T, E));
+    const int rc = router_forward_args(name, a, blocks, logits, dtype, T, E, ld, topk, token_mask, score, renorm, scale, loss_coef,
                                  topk_idx, weights, counts, loss, workspace, ws_bytes);
     if (rc != FGB_OK)
         return rc;
@@ -408,7 +408,7 @@ extern "C" int moe_router_grouped(const void *logits, int dtype, int64_t T, int 
         score == FGB_ROUTER_SOFTMAX ? launch_grouped<false, FGB_ROUTER_SOFTMAX>(a, st)
                                     : launch_grouped<false, FGB_ROUTER_SIGMOID>(a, st);
     FGB_LAUNCHED("router_grouped_kernel");
-    return router_finish(a, st);
+    return router_finish(a, blocks, st);
 }
 
 extern "C" int moe_bias_update(const float *bias, const int32_t *counts, int E, float rate, float *out, void *stream)

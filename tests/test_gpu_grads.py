@@ -61,7 +61,7 @@ def test_sizes_and_types(kind, clipped):
     check(grads, most, in_place=True)
 
 
-@pytest.mark.parametrize("n", [1, 119, 120, 121, 240, 241, 500])
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 119, 120, 121, 165, 166, 167, 240, 241, 332, 333, 500])
 def test_many_tensors(n):
     print("[case] tensors", n, flush=True)
     rng = np.random.default_rng(n)
@@ -178,3 +178,13 @@ def test_past_four_gib():
     norm = fgb().grad_clip([g], 1.0)
     assert float(norm) == 4.0
     assert g[-3:].tolist() == [0.5] * 3 and float(g[0]) == 0.5 and float(g[1]) == 0 and float(g[-4]) == 0
+
+
+@pytest.mark.parametrize("chunks", [1, 255, 256, 257, 2047, 2049])
+def test_norm_is_the_sumsq_s(chunks):
+    """The norm that clipping forms itself and the one from grad_sumsq's result, bit for bit, few parts and many."""
+    g = make([chunks * 8192 - 5, 3], [BF16, F32], chunks)
+    outs = [torch.empty_like(v) for v in g]
+    a = fgb().grad_clip(g, 0.5, out=outs)
+    b = fgb().grad_clip(g, 0.5, out=[torch.empty_like(v) for v in g], sumsq=fgb().grad_sumsq(g))
+    assert torch.equal(a, b)

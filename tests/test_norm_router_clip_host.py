@@ -202,3 +202,46 @@ def test_binding_refuses():
             call([torch.zeros(4)])
         with pytest.raises(ValueError, match="empty"):
             call([])
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """A launch goes to the current device, so a call for another one makes that current."""
+    import fine_grained_blockwise_amd as fgb
+    seen = []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            seen.append(("enter", self.d.index))
+
+        def __exit__(self, *a):
+            seen.append(("exit", self.d.index))
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(fgb, "_current_device", lambda: 1)
+    monkeypatch.setattr(fgb, "_call", lambda *a: seen.append(a))
+    fgb._call_on(torch.device("cuda", 1), "f", 2)
+    assert seen == [("f", 2)]
+    fgb._call_on(torch.device("cuda", 0), "g", 3)
+    assert seen[1:] == [("enter", 0), ("g", 3), ("exit", 0)]
+
+
+def test_tensor_helper():
+    import fine_grained_blockwise_amd as fgb
+    t = fgb._tensors
+    a = t.empties(torch.zeros(2), (0, 3, 4), (1, 5), (2,), (3, 0, 2, 3))
+    assert [(v.dtype, tuple(v.shape)) for v in a] == [(torch.float32, (3, 4)), (torch.bfloat16, (5,)),
+                                                      (torch.uint8, ()), (torch.int32, (0, 2, 3))]
+    for bad in ((torch.zeros(1), 3), (3,), (), (torch.zeros(1), ()), (torch.zeros(1), (0, 1, 1, 1, 1)), (torch.zeros(1), ("x",))):
+        with pytest.raises(TypeError):
+            t.empties(*bad)
+    for bad in ((4, 1), (0, -1)):
+        with pytest.raises(ValueError):
+            t.empties(torch.zeros(1), bad)
+    with pytest.raises(RuntimeError):
+        t.empties(torch.zeros(1), (0, 1 << 62, 1 << 62))
+    assert t.describe([]) == (b"", b"", b"", -1)
+    for bad in (3, [torch.zeros(1), None], [object()]):
+        with pytest.raises((TypeError, ValueError)):
+            t.describe(bad)

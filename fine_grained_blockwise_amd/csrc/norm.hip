@@ -8,8 +8,8 @@
 //   dx = dh + rstd (a - hat mean_c(a hat)), dw = sum over the rows of dy hat.
 //
 // Both are bound by memory: every input is read once, into registers, and every output
-// written once.  A row belongs to W waves (1, 4 or 16: columns up to 2048, 8192, 32768),
-// a lane holds up to four chunks of eight neighbouring columns, so the row's sum, the
+// written once.  A row belongs to W waves (1, 4, 8 or 16: columns up to 2048, 8192, 16384,
+// 32768), a lane holds up to four chunks of eight neighbouring columns, so the row's sum, the
 // groups' amax (16 or 4 neighbouring lanes) and the outputs all come from one read.
 #include "fgb_internal.h"
 
@@ -43,9 +43,14 @@ template <bool BF16> __device__ __forceinline__ Raw8<BF16> load8(const void *p, 
 {
     Raw8<BF16> o;
     const uint8_t *b = (const uint8_t *)p + at * (BF16 ? 2 : 4);
-    o.v[0] = ld_stream16(b);
-    if constexpr (!BF16)
-        o.v[1] = ld_stream16(b + 16);
+    // (FP32: the lanes' first and second halves lie in the same lines, which the second load
+    // finds in the cache: 4096 x 7168 58.5 us past it, 54.5 so)
+    if constexpr (BF16) {
+        o.v[0] = ld_stream16(b);
+    } else {
+        o.v[0] = *reinterpret_cast<const uint4 *>(b);
+        o.v[1] = *reinterpret_cast<const uint4 *>(b + 16);
+    }
     return o;
 }
 template <bool BF16> __device__ __forceinline__ void widen(const Raw8<BF16> &o, float (&f)[8])
@@ -207,62 +212,113 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_kernel(NormArgs a)
     }
 }
 
+// A row's gradient from registers.
+template <bool HBF> __device__ __forceinline__ void store_dx(const NormGradArgs &a, int64_t at, const float (&d)[8],
+                                                             const float (&h)[8], const float (&e)[8], float rstd, float mean)
+{
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        o[i] = fmaf(rstd, fmaf(h[i], -mean, d[i]), e[i]);
+    store8<HBF>(a.dx, at, narrow<HBF>(o));
+}
+
+// Sixteen waves have 128 registers a lane, which a row and its part of dw do not fit: they read
+// the row again after the sum (4096 x 32768: 286 us, from registers that spill 720).
 template <bool DBF, bool HBF, int W, int CH>
 __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_grad_kernel(NormGradArgs a)
 {
+    constexpr bool AGAIN = W == 16;
     __shared__ float red[2][16];
     const int t = threadIdx.x % (64 * W);
     const int64_t first = (int64_t)blockIdx.x * NORM_ROWS<W> + (W == 1 ? threadIdx.x >> 6 : 0);
     if (W == 1 && first >= a.parts) // (a whole wave, and no barrier follows)
         return;
-    float w[CH][8], dw[CH][8];
-    Raw8<DBF> rd[CH];
-    Raw8<HBF> rh[CH], re[CH];
+    float w[AGAIN ? 1 : CH][8], dw[CH][8];
 #pragma unroll
     for (int u = 0; u < CH; u++) {
         const int c = chunk_col<W>(u, t);
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            w[u][i] = dw[u][i] = 0.0f; // (columns past the last one add nothing)
-        if (c < a.cols)
-            load_weight(a.w, a.w_bf16, c, w[u]);
+        for (int i = 0; i < 8; i++) {
+            dw[u][i] = 0.0f;
+            if constexpr (!AGAIN)
+                w[u][i] = 0.0f; // (columns past the last one add nothing)
+        }
+        if constexpr (!AGAIN)
+            if (c < a.cols)
+                load_weight(a.w, a.w_bf16, c, w[u]);
     }
     int odd = 0;
     for (int64_t row = first; row < a.rows; row += a.parts) {
         const float rstd = a.rstd[row];
-        load_row<DBF, W>(rd, a.dy, row * a.lddy, a.cols, t);
-        load_row<HBF, W>(rh, a.h, row * a.ldh, a.cols, t);
-        if (a.dh)
-            load_row<HBF, W>(re, a.dh, row * a.lddh, a.cols, t);
-        float d[CH][8], h[CH][8], e[CH][8];
         float sum = 0.0f;
+        if constexpr (AGAIN) {
+#pragma unroll 1
+            for (int u = 0; u < CH; u++) {
+                const int c = chunk_col<W>(u, t);
+                if (c < a.cols) {
+                    float d[8], h[8];
+                    widen<DBF>(load8<DBF>(a.dy, row * a.lddy + c), d);
+                    widen<HBF>(load8<HBF>(a.h, row * a.ldh + c), h);
+                    load_weight(a.w, a.w_bf16, c, w[0]);
 #pragma unroll
-        for (int u = 0; u < CH; u++) {
-            widen<DBF>(rd[u], d[u]);
-            widen<HBF>(rh[u], h[u]);
-            if (a.dh)
-                widen<HBF>(re[u], e[u]);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                h[u][i] *= rstd;
-                dw[u][i] = fmaf(d[u][i], h[u][i], dw[u][i]);
-                d[u][i] *= w[u][i];
-                sum = fmaf(d[u][i], h[u][i], sum);
-                if (!a.dh)
-                    e[u][i] = 0.0f;
+                    for (int i = 0; i < 8; i++)
+                        sum = fmaf(d[i] * w[0][i], h[i] * rstd, sum);
+                }
             }
-        }
-        const float mean = row_sum<W>(sum, red[odd]) / (float)a.cols;
-        odd ^= 1;
+            const float mean = row_sum<W>(sum, red[odd]) / (float)a.cols;
+            odd ^= 1;
 #pragma unroll
-        for (int u = 0; u < CH; u++) {
-            const int c = chunk_col<W>(u, t);
-            if (c < a.cols) {
-                float o[8];
+            for (int u = 0; u < CH; u++) {
+                const int c = chunk_col<W>(u, t);
+                if (c < a.cols) {
+                    float d[8], h[8], e[8] = {};
+                    widen<DBF>(load8<DBF>(a.dy, row * a.lddy + c), d);
+                    widen<HBF>(load8<HBF>(a.h, row * a.ldh + c), h);
+                    if (a.dh)
+                        widen<HBF>(load8<HBF>(a.dh, row * a.lddh + c), e);
+                    load_weight(a.w, a.w_bf16, c, w[0]);
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    o[i] = fmaf(rstd, fmaf(h[u][i], -mean, d[u][i]), e[u][i]);
-                store8<HBF>(a.dx, row * a.lddx + c, narrow<HBF>(o));
+                    for (int i = 0; i < 8; i++) {
+                        h[i] *= rstd;
+                        dw[u][i] = fmaf(d[i], h[i], dw[u][i]);
+                        d[i] *= w[0][i];
+                    }
+                    store_dx<HBF>(a, row * a.lddx + c, d, h, e, rstd, mean);
+                }
+                __builtin_amdgcn_sched_barrier(0); // (a chunk at a time, for its registers)
+            }
+        } else {
+            Raw8<DBF> rd[CH];
+            Raw8<HBF> rh[CH], re[CH];
+            load_row<DBF, W>(rd, a.dy, row * a.lddy, a.cols, t);
+            load_row<HBF, W>(rh, a.h, row * a.ldh, a.cols, t);
+            if (a.dh)
+                load_row<HBF, W>(re, a.dh, row * a.lddh, a.cols, t);
+            float d[CH][8], h[CH][8], e[CH][8];
+#pragma unroll
+            for (int u = 0; u < CH; u++) {
+                widen<DBF>(rd[u], d[u]);
+                widen<HBF>(rh[u], h[u]);
+                if (a.dh)
+                    widen<HBF>(re[u], e[u]);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    h[u][i] *= rstd;
+                    dw[u][i] = fmaf(d[u][i], h[u][i], dw[u][i]);
+                    d[u][i] *= w[u][i];
+                    sum = fmaf(d[u][i], h[u][i], sum);
+                    if (!a.dh)
+                        e[u][i] = 0.0f;
+                }
+            }
+            const float mean = row_sum<W>(sum, red[odd]) / (float)a.cols;
+            odd ^= 1;
+#pragma unroll
+            for (int u = 0; u < CH; u++) {
+                const int c = chunk_col<W>(u, t);
+                if (c < a.cols)
+                    store_dx<HBF>(a, row * a.lddx + c, d[u], h[u], e[u], rstd, mean);
             }
         }
     }
@@ -304,13 +360,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(NormGradArgs a)
     }
 }
 
-static int norm_waves(int64_t cols) { return cols <= 2048 ? 1 : cols <= 8192 ? 4 : 16; }
+static int norm_waves(int64_t cols) { return cols <= 2048 ? 1 : cols <= 8192 ? 4 : cols <= 16384 ? 8 : 16; }
 static bool norm_two_chunks(int64_t cols) { return cols <= 1024 * norm_waves(cols); }
 
-// Rows that add up separately for dw: enough for two workgroups a CU.
+// Rows that add up separately for dw: a wave's, or a workgroup's for two a CU (more than 8192
+// columns: one; 4096 x 16384 97 + 5 us, with two 102 + 7).
 static int64_t norm_parts(int64_t rows, int64_t cols)
 {
-    const int64_t most = norm_waves(cols) == 1 ? 2048 : 512;
+    const int64_t most = norm_waves(cols) == 1 ? 2048 : cols <= 8192 ? 512 : 256;
     return rows < 1 ? 1 : rows < most ? rows : most;
 }
 
@@ -341,8 +398,11 @@ static int check_rows(const char *name, const char *what, const void *p, int dty
         case 4:                                                                                                        \
             if (two_) { LAUNCH(4, 2); } else { LAUNCH(4, 4); }                                                         \
             break;                                                                                                     \
+        case 8:                                                                                                        \
+            LAUNCH(8, 4);                                                                                              \
+            break;                                                                                                     \
         default:                                                                                                       \
-            if (two_) { LAUNCH(16, 2); } else { LAUNCH(16, 4); }                                                       \
+            LAUNCH(16, 4);                                                                                             \
         }                                                                                                              \
     } while (0)
 

@@ -180,7 +180,7 @@ def test_backward(rows, cols, dt, ht, wt, add):
                    w, rows_of((rows, cols), 3, ht, 1e-3) if add else None)
 
 
-@pytest.mark.parametrize("rows,cols", [(2049, 512), (4099, 7168), (8195, 64), (2500, 1536)])
+@pytest.mark.parametrize("rows,cols", [(2049, 512), (4099, 7168), (8195, 64), (2500, 1536), (519, 8224), (263, 20480)])
 def test_backward_many_rows(rows, cols):
     print("[case] rmsnorm_backward", rows, cols, flush=True)
     check_backward(rows_of((rows, cols), 1, BF16, 1e-3), rows_of((rows, cols), 2, BF16), torch.ones(cols, dtype=BF16),
@@ -242,3 +242,17 @@ def test_rows_past_two_to_the_31_elements():
     dx, dw = fgb().rmsnorm_backward(x, x, w, rstd)
     one, _ = fgb().rmsnorm_backward(x[-1000:], x[-1000:], w, rstd[-1000:])
     assert torch.equal(dx[-1000:], one)
+
+
+@pytest.mark.parametrize("cols", [512, 7168, 16384, 20480])
+def test_backward_in_place_over_every_width(cols):
+    """dx over dy and over dh, more rows than parts."""
+    rows = 2100 if cols <= 2048 else 530
+    w = (1 + 0.3 * torch.randn(cols, generator=torch.Generator().manual_seed(3))).to(BF16).to(DEV)
+    dy, h, dh = (rows_of((rows, cols), i, BF16).to(DEV) for i in (1, 2, 3))
+    rstd = (1 / torch.sqrt(h.double().square().mean(1) + 1e-6)).float()
+    want = fgb().rmsnorm_backward(dy, h, w, rstd, dh=dh)
+    for k in range(2):
+        t = [dy.clone(), h, dh.clone()]
+        got = fgb().rmsnorm_backward(t[0], t[1], w, rstd, dh=t[2], dx=t[2 * k])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -11,6 +11,11 @@
 // written once.  A row belongs to W waves (1, 4, 8 or 16: columns up to 2048, 8192, 16384,
 // 32768), a lane holds up to four chunks of eight neighbouring columns, so the row's sum, the
 // groups' amax (16 or 4 neighbouring lanes) and the outputs all come from one read.
+// 8192 x 7168 BF16: forward 70 us (5.9 TB/s), gradient 78 us (6.0 TB/s) and 5 us for dw.
+//
+// Loads are streaming, stores ordinary: with streaming ones the gradient took 85 us, the
+// forward and a reader of its codes 103 (96 so).  A row's loads go out together, without
+// branches; waiting for each chunk in turn the gradient took 146 us.
 #include "fgb_internal.h"
 
 namespace fgb {
@@ -410,7 +415,8 @@ template <bool XBF, bool HBF, bool RES> static void launch_norm(const NormArgs &
 {
 #define FGB_N(W, CH)                                                                                                   \
     do {                                                                                                               \
-        const int64_t n = (a.rows + NORM_ROWS<W> - 1) / NORM_ROWS<W>;                                                  \
+        const int64_t n = (a.rows + NORM_ROWS<W> - 1) / NORM_ROWS<W>; /* eight workgroups a CU take rows in turn:   */ \
+        /* 8192 x 7168 with a reader of the codes 96 us, a workgroup a row 101.5, 1536 of them 107 */                  \
         rmsnorm_kernel<XBF, HBF, RES, W, CH>                                                                           \
             <<<(unsigned)(n < 2048 ? n : 2048), NORM_THREADS<W>, 0, st>>>(a);                                          \
     } while (0)

@@ -8,7 +8,8 @@
 // values: the lowest id) cannot be chosen.
 //
 // L lanes take a token and hold its experts as in router_device.h.  Bound by instruction issue:
-// 16384 x 256 logits are 17 MB.
+// 16384 x 256 logits are 17 MB, and choosing 8 in 4 of 8 groups with the loss takes 20 us (28
+// under a trace), of which the FP64 scores 4, the groups 3, the rounds of the choice 4.
 #include "router_device.h"
 
 namespace fgb {

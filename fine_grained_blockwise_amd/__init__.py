@@ -355,12 +355,14 @@ def fp8_dequant(q, s, gran, out_dtype=torch.float32):
     """decode(q) * 2^(s-127) -> out [rows, cols] (fp32 or bf16); q, s dense."""
     _check_2d_codes(q, "fp8_dequant: q")
     rows, cols = q.shape
-    _need(s, "fp8_dequant: s", shape=_scale_shape(rows, cols, gran), dtype=torch.uint8)
+    if not _all_u8((q, q.shape), (s, _scale_shape(rows, cols, gran))):
+        _need(s, "fp8_dequant: s", shape=_scale_shape(rows, cols, gran), dtype=torch.uint8)
+        q, s = q.contiguous(), s.contiguous()
     _out_dtype(out_dtype, "fp8_dequant")
     _check_dev(q, s)
-    out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
-    _call("fp8_dequant", _ptr(q.contiguous()), _ptr(s.contiguous()), gran, rows, cols, _ptr(out),
-          _dtype_code(out), _stream(q))
+    code = _CODES[out_dtype]
+    out, = _tensors.empties(q, (code, rows, cols))
+    _call("fp8_dequant", q.data_ptr(), s.data_ptr(), gran, rows, cols, out.data_ptr(), code, _stream(q))
     return out
 
 

@@ -188,3 +188,9 @@ def test_norm_is_the_sumsq_s(chunks):
     a = fgb().grad_clip(g, 0.5, out=outs)
     b = fgb().grad_clip(g, 0.5, out=[torch.empty_like(v) for v in g], sumsq=fgb().grad_sumsq(g))
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("sizes", [[1] * 166 + [0] * 3, [0] * 3 + [1] * 166, [0] * 170 + [4] + [0] * 170, [9] * 332 + [0]])
+def test_empty_tensors_around_a_full_list(sizes):
+    grads = make(sizes, [F32 if i % 3 else BF16 for i in range(len(sizes))], 11)
+    check(grads, 1e-3, in_place=True)

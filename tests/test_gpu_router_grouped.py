@@ -200,3 +200,15 @@ def test_bias_update(E):
     bd, cd = b.to(DEV), torch.from_numpy(counts).to(DEV)
     assert torch.equal(fgb().moe_bias_update(bd, cd, 1e-3).cpu(), want)
     assert fgb().moe_bias_update(bd, cd, 1e-3, out=bd) is bd and torch.equal(bd.cpu(), want)
+
+
+@pytest.mark.parametrize("T,E,k,G,kg", [
+    (9001, 128, 8, 64, 20), (9001, 64, 8, 16, 5), (9001, 256, 8, 64, 17), (5001, 512, 8, 4, 2), (9001, 96, 4, 2, 1),
+    (3, 2, 1, 2, 1), (5, 3, 2, 3, 2), (300, 3, 1, 1, 1), (9000, 9, 3, 3, 2), (4500, 768, 7, 48, 11),
+])
+def test_group_shapes_over_many_tokens(T, E, k, G, kg):
+    """Every way a group's two largest are found, with few and many lanes a token and up to 64 groups."""
+    print("[case] group shapes", T, E, k, G, kg, flush=True)
+    for biased, score, dtype in ((True, R.SIGMOID, F32), (False, R.SOFTMAX, BF16), (True, R.SOFTMAX, BF16)):
+        if biased or G > 1:
+            check(logits(T, E, E, dtype), k, biases(E, 3) if biased else None, G, kg, score, True)

@@ -360,6 +360,12 @@ __global__ __launch_bounds__(256) void router_bwd_kernel(RouterArgs a)
             const float total = group_sum<L>(chosen);
             inv = 1.0f / total;
             mean = dv * inv;
+            // A lone expert's weight is constant: its part is 0, not what v (1 / v) D - D leaves,
+            // which can outweigh the loss's part.
+            const uint64_t slots = __ballot(slot >= 0) >> ((threadIdx.x & 63) & ~(L - 1));
+            const bool lone = __builtin_popcountll(L == 64 ? slots : slots & ((1ull << (L & 63)) - 1)) == 1;
+            inv = lone ? 0.0f : inv;
+            mean = lone ? 0.0f : mean;
             far = live && total < FAR;
             any_far |= __any(far) != 0;
         }

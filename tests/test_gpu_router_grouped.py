@@ -212,3 +212,28 @@ def test_group_shapes_over_many_tokens(T, E, k, G, kg):
     for biased, score, dtype in ((True, R.SIGMOID, F32), (False, R.SOFTMAX, BF16), (True, R.SOFTMAX, BF16)):
         if biased or G > 1:
             check(logits(T, E, E, dtype), k, biases(E, 3) if biased else None, G, kg, score, True)
+
+
+@pytest.mark.parametrize("score", [R.SOFTMAX, R.SIGMOID])
+@pytest.mark.parametrize("E,k", [(432, 1), (32, 1), (100, 4), (700, 12), (64, 40)])
+def test_a_lone_expert_s_weight_is_constant(E, k, score):
+    """Renormed, the weight of a token's only expert is 1 whatever its logit: gradients of the weights add nothing, bit
+    for bit, where one slot was filled."""
+    T = 300
+    z = logits(T, E, E)
+    g = torch.Generator().manual_seed(5)
+    only = torch.randint(0, E, (T,), generator=g)
+    if k > 1:
+        z[::2] = -np.inf
+        z[torch.arange(0, T, 2), only[::2]] = 0.5
+    zd = z.to(DEV)
+    how = dict(score=score, renorm=True, scale=2.5, loss_coef=0.01)
+    idx, w, counts, _ = fgb().moe_router(zd, k, bias=biases(E, 2).to(DEV), **how)
+    dw = torch.randn(T, k, generator=g).to(DEV)
+    one = torch.ones((), device=DEV)
+    with_w = fgb().moe_router_backward(zd, idx, counts, dw, one, **how)
+    without = fgb().moe_router_backward(zd, idx, counts, None, one, **how)
+    rows = slice(None) if k == 1 else slice(0, None, 2)
+    assert torch.equal(with_w[rows], without[rows]) and (w[rows, 0] == 2.5).all()
+    if k > 1:
+        assert not torch.equal(with_w[1::2], without[1::2])

@@ -237,3 +237,24 @@ def test_a_lone_expert_s_weight_is_constant(E, k, score):
     assert torch.equal(with_w[rows], without[rows]) and (w[rows, 0] == 2.5).all()
     if k > 1:
         assert not torch.equal(with_w[1::2], without[1::2])
+
+
+def test_logits_past_two_to_the_31():
+    """More than 2^31 logits: the last tokens as if alone (1024 experts have the same lanes in both calls)."""
+    T, E, k = 2 ** 21 + 77, 1024, 8
+    z = torch.empty(T, E, dtype=BF16, device=DEV)
+    part = logits(4096, E, 1, BF16).to(DEV)
+    for lo in range(0, T, 4096):
+        z[lo: lo + 4096].copy_(part[: min(4096, T - lo)])
+    z[-50:].copy_(logits(50, E, 2, BF16))
+    how = dict(score=R.SIGMOID, renorm=True, scale=2.5, loss_coef=0.01)
+    choice = dict(bias=biases(E, 1).to(DEV), groups=8, topk_groups=4)
+    idx, w, counts, loss = fgb().moe_router(z, k, **how, **choice)
+    one = fgb().moe_router(z[-50:], k, **how, **choice)
+    assert torch.equal(idx[-50:], one[0]) and torch.equal(w[-50:], one[1])
+    assert int(counts[E]) == T and int(counts[:E].sum()) == T * k and float(loss) > 0
+    dw = torch.ones(T, k, device=DEV)
+    dw[:, 0] = 0.5
+    dz = fgb().moe_router_backward(z, idx, counts, dw, torch.ones((), device=DEV), **how)
+    few = fgb().moe_router_backward(z[-50:], idx[-50:], counts, dw[-50:], torch.ones((), device=DEV), **how)
+    assert torch.equal(dz[-50:], few)

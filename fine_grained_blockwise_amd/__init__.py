@@ -1256,19 +1256,28 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
         raise ValueError(f"{name}: eps must be positive")
     if h is not None and residual is None:
         raise ValueError(f"{name}: h needs a residual")
-    x, x_code, ldx = _norm_rows(x, "rmsnorm_quant: x")
-    rows, cols = shape = x.shape
-    _norm_cols(cols, name)
+    usual = _tensors.usual(x, weight, residual)
+    if usual is not None:
+        rows, cols, x_at, x_code, w_at, w_code, r_at, r_code = usual
+        ldx = ldr = cols
+        _norm_cols(cols, name)
+        if h is not None:
+            _check_dev(x, h)
+    else:
+        x, x_code, ldx = _norm_rows(x, f"{name}: x")
+        rows, cols = x.shape
+        _norm_cols(cols, name)
+        weight, w_code = _norm_weight(weight, cols, name)
+        ldr, r_code = cols, F32
+        if residual is not None:
+            residual, r_code, ldr = _norm_rows(residual, f"{name}: residual", x.shape)
+        _check_dev(x, weight, residual, h)
+        x_at, w_at, r_at = x.data_ptr(), weight.data_ptr(), _ptr(residual)
+    dev, ldh = x.device, cols
     if quant and cols % group:
         raise ValueError(f"{name}: cols ({cols}) must be a multiple of the group ({group})")
-    weight, w_code = _norm_weight(weight, cols, name)
-    ldr = ldh = cols
-    r_code = F32
-    if residual is not None:
-        residual, r_code, ldr = _norm_rows(residual, "rmsnorm_quant: residual", shape)
-        if h is not None:
-            ldh = _norm_out(h, f"{name}: h", shape, residual.dtype)
-    dev = _check_dev(x, weight, residual, h)
+    if h is not None:
+        ldh = _norm_out(h, f"{name}: h", (rows, cols), residual.dtype)
     if quant and y_dtype is None and h is None and residual is not None:  # the usual outputs in one call
         y = None
         h, q, s, rstd = _tensors.empties(x, (r_code, rows, cols), (_KU8, rows, cols), (_KU8, rows, cols // group),
@@ -1282,9 +1291,8 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
             y, = _tensors.empties(x, (_CODES[_out_dtype(y_dtype, name)], rows, cols))
         if quant:
             q, s = _tensors.empties(x, (_KU8, rows, cols), (_KU8, rows, cols // group))
-    _call_on(dev, name, x.data_ptr(), x_code, rows, cols, ldx, _ptr(residual), r_code, ldr, weight.data_ptr(), w_code,
-             eps, group, _ptr(h), ldh, rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype],
-             cols, _stream(x))
+    _call_on(dev, name, x_at, x_code, rows, cols, ldx, r_at, r_code, ldr, w_at, w_code, eps, group, _ptr(h), ldh,
+             rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype], cols, _stream(x))
     return q, s, y, x if h is None else h, rstd
 
 
@@ -1299,21 +1307,35 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
     dx is the gradient of h, and so of x and the residual, with dh (what reaches h past the norm, in h's dtype) added
     before its rounding; dx= takes a tensor for it, which may be dh or dy itself."""
     name = "rmsnorm_backward"
-    dy, dy_code, lddy = _norm_rows(dy, "rmsnorm_backward: dy")
-    rows, cols = shape = dy.shape
-    _norm_cols(cols, name)
-    h, h_code, ldh = _norm_rows(h, "rmsnorm_backward: h", shape)
-    weight, w_code = _norm_weight(weight, cols, name)
+    usual = _tensors.usual(dy, weight, h, dh)
+    if usual is not None:
+        rows, cols, dy_at, dy_code, w_at, w_code, h_at, h_code, dh_at, _ = usual
+        lddy = ldh = lddh = cols
+        _norm_cols(cols, name)
+        if dh is not None and dh.dtype is not h.dtype:
+            _need(dh, f"{name}: dh", dtype=h.dtype)
+    else:
+        dy, dy_code, lddy = _norm_rows(dy, f"{name}: dy")
+        rows, cols = dy.shape
+        _norm_cols(cols, name)
+        h, h_code, ldh = _norm_rows(h, f"{name}: h", dy.shape)
+        weight, w_code = _norm_weight(weight, cols, name)
+        lddh = cols
+        if dh is not None:
+            _need(dh, f"{name}: dh", dtype=h.dtype)
+            dh, _, lddh = _norm_rows(dh, f"{name}: dh", dy.shape)
+        dy_at, w_at, h_at, dh_at = dy.data_ptr(), weight.data_ptr(), h.data_ptr(), _ptr(dh)
     _need(rstd, f"{name}: rstd", shape=(rows,), dtype=torch.float32, contiguous=True)
-    lddh = lddx = cols
-    if dh is not None:
-        _need(dh, "rmsnorm_backward: dh", dtype=h.dtype)
-        dh, _, lddh = _norm_rows(dh, "rmsnorm_backward: dh", shape)
+    lddx = cols
     if dx is not None:
-        lddx = _norm_out(dx, f"{name}: dx", shape, h.dtype)
+        lddx = _norm_out(dx, f"{name}: dx", (rows, cols), h.dtype)
     if workspace is not None:
         _need(workspace, f"{name}: workspace", dtype=_U8, contiguous=True)
-    dev = _check_dev(dy, h, weight, rstd, dh, dx, workspace)
+    if usual is None or dx is not None or workspace is not None:
+        _check_dev(dy, h, weight, rstd, dh, dx, workspace)
+    else:
+        _check_dev(dy, rstd)
+    dev = dy.device
     need = (_KU8, _lib.rmsnorm_backward_workspace_size(rows, cols))
     if dx is None and workspace is None:
         dx, workspace, dweight = _tensors.empties(dy, (h_code, rows, cols), need, (F32, cols))
@@ -1323,8 +1345,8 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
             dx, = _tensors.empties(dy, (h_code, rows, cols))
         if workspace is None:
             workspace, = _tensors.empties(dy, need)
-    _call_on(dev, name, dy.data_ptr(), dy_code, rows, cols, lddy, h.data_ptr(), h_code, ldh,
-             weight.data_ptr(), w_code, rstd.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), lddx,
+    _call_on(dev, name, dy_at, dy_code, rows, cols, lddy, h_at, h_code, ldh, w_at, w_code, rstd.data_ptr(), dh_at, lddh,
+             dx.data_ptr(), lddx,
              dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dy))
     return dx, dweight
 

@@ -9,6 +9,11 @@
 // empties(tensor, (kind, sizes...), ...) -> uninitialised tensors on the given one's device, of
 // kind 0 float32, 1 bfloat16, 2 uint8, 3 int32.  (torch.empty costs 1.3 us from Python, 0.5 us
 // here.)
+//
+// usual(matrix, vector, matrices...) -> (rows, cols, address and type of each, 0 and FGB_F32 for
+// None) where all are as the calls mostly have them: FP32 or BF16, on one GPU, contiguous and
+// 16-byte aligned, the matrices of one shape [rows, cols], the vector [cols].  None where
+// anything is not: the caller then looks for what it is.  (3 us in Python, 0.3 us here.)
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -84,9 +89,61 @@ static PyObject *empties(PyObject *, PyObject *const *args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// Whether t is an FP32 or BF16 tensor on GPU `device` (-1: any, which it then is), contiguous and
+// 16-byte aligned.
+static bool is_usual(const at::Tensor &t, long &device)
+{
+    if (!t.is_cuda() || t.layout() != at::kStrided || (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16))
+        return false;
+    const long on = t.get_device();
+    if (device < 0)
+        device = on;
+    return on == device && t.is_contiguous() && ((uintptr_t)t.data_ptr() & 15) == 0;
+}
+
+static PyObject *usual(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n < 2)
+        return PyErr_Format(PyExc_TypeError, "usual: expected a matrix and a vector");
+    for (Py_ssize_t i = 0; i < n; i++)
+        if (!THPVariable_Check(args[i]) && !(i > 1 && args[i] == Py_None))
+            Py_RETURN_NONE;
+    const at::Tensor &m = THPVariable_Unpack(args[0]), &v = THPVariable_Unpack(args[1]);
+    long device = -1;
+    if (!is_usual(m, device) || m.dim() != 2 || !is_usual(v, device) || v.dim() != 1 || v.size(0) != m.size(1))
+        Py_RETURN_NONE;
+    for (Py_ssize_t i = 2; i < n; i++)
+        if (args[i] != Py_None) {
+            const at::Tensor &t = THPVariable_Unpack(args[i]);
+            if (!is_usual(t, device) || t.sizes() != m.sizes())
+                Py_RETURN_NONE;
+        }
+    THPObjectPtr out(PyTuple_New(2 + 2 * n));
+    if (!out)
+        return nullptr;
+    const auto put = [&](Py_ssize_t at, long long value) {
+        PyObject *o = PyLong_FromLongLong(value);
+        if (o)
+            PyTuple_SET_ITEM(out.get(), at, o);
+        return o != nullptr;
+    };
+    if (!put(0, m.size(0)) || !put(1, m.size(1)))
+        return nullptr;
+    for (Py_ssize_t i = 0; i < n; i++) {
+        const bool none = args[i] == Py_None;
+        if (!put(2 + 2 * i, none ? 0 : (long long)(uintptr_t)THPVariable_Unpack(args[i]).data_ptr()) ||
+            !put(3 + 2 * i, none || THPVariable_Unpack(args[i]).scalar_type() == at::kFloat ? FGB_F32 : FGB_BF16))
+            return nullptr;
+    }
+    return out.release();
+    END_HANDLE_TH_ERRORS
+}
+
 static PyMethodDef methods[] = {
     {"describe", describe, METH_O, "addresses, lengths, types and device of a list of tensors"},
     {"empties", (PyCFunction)(void (*)(void))empties, METH_FASTCALL, "uninitialised tensors on a tensor's device"},
+    {"usual", (PyCFunction)(void (*)(void))usual, METH_FASTCALL, "sizes, addresses and types of tensors laid out as usual"},
     {nullptr, nullptr, 0, nullptr}};
 static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

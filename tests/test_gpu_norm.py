@@ -256,3 +256,25 @@ def test_backward_in_place_over_every_width(cols):
         t = [dy.clone(), h, dh.clone()]
         got = fgb().rmsnorm_backward(t[0], t[1], w, rstd, dh=t[2], dx=t[2 * k])
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_usual_tensors():
+    """What the binding's helper says of tensors, and that it leaves everything else to the checks."""
+    usual = fgb()._tensors.usual
+    x, w = torch.zeros(4, 96, device=DEV, dtype=BF16), torch.zeros(97, device=DEV)
+    r = torch.zeros(4, 96, device=DEV)
+    assert usual(x, w[:96], r, None) == (4, 96, x.data_ptr(), 1, w.data_ptr(), 0, r.data_ptr(), 0, 0, 0)
+    wide = torch.zeros(4, 104, device=DEV)
+    for bad in ((x, w), (x, w[1:]), (x, w[:96], wide[:, :96]), (x, w[:96], r.t()), (x, w[:96], r.half()), (x, w[:96], r[0]),
+                (x[:, 1:], w[:95]), (x, w[:96], r.cpu()), (x, r), (r[0], w[:96]), (x, w[:96], 3), (x, None)):
+        assert usual(*bad) is None
+    with pytest.raises(ValueError, match="dh"):
+        fgb().rmsnorm_backward(x, r, w[:96], torch.ones(4, device=DEV), dh=x)
+    with pytest.raises(ValueError, match="same GPU|on the GPU"):
+        fgb().rmsnorm_backward(x, r, w[:96], torch.ones(4))
+    with pytest.raises(ValueError, match="on the GPU"):
+        fgb().rmsnorm_quant(x, w[:96], residual=r, group=32, h=r.cpu())
+    with pytest.raises(ValueError, match="must have shape"):
+        fgb().rmsnorm_quant(x, w[:96], residual=r[:3], group=32)
+    with pytest.raises(ValueError, match="weight"):
+        fgb().rmsnorm_quant(x, w, group=32)

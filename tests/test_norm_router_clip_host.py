@@ -241,6 +241,9 @@ def test_tensor_helper():
             t.empties(torch.zeros(1), bad)
     with pytest.raises(RuntimeError):
         t.empties(torch.zeros(1), (0, 1 << 62, 1 << 62))
+    assert t.usual(torch.zeros(2, 3), torch.zeros(3), None) is None and t.usual(None, torch.zeros(3)) is None  # (no GPU)
+    with pytest.raises(TypeError):
+        t.usual(torch.zeros(2, 3))
     assert t.describe([]) == (b"", b"", b"", -1)
     for bad in (3, [torch.zeros(1), None], [object()]):
         with pytest.raises((TypeError, ValueError)):

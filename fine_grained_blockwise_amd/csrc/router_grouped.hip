@@ -123,8 +123,10 @@ __device__ __forceinline__ void close_groups(const GroupedArgs &a, uint32_t (&ke
                                              int e0, uint32_t *values, uint32_t *keys)
 {
     constexpr int R = 4 * Q;
-    const auto value = [&](uint32_t first, uint32_t second) { // (keys > 0 are neither -inf nor NaN)
-        return a.bias && second ? logit_key<false>(key_logit<false>(first) + key_logit<false>(second), 0) : first;
+    // (Keys > 0 are neither -inf nor NaN.  The sum of two of them can be -inf, whose key is 0: it
+    // gets the key below the finite ones, as 0 is a group's that has nothing to choose.)
+    const auto value = [&](uint32_t first, uint32_t second) {
+        return a.bias && second ? max(logit_key<false>(key_logit<false>(first) + key_logit<false>(second), 0), 1u) : first;
     };
     if (a.lanes > 0) { // uniform
 #pragma unroll

@@ -714,8 +714,10 @@ int moe_router_backward(const void *logits, int dtype, int64_t T, int E, int64_t
  *   groups, topk_groups : the experts are `groups` runs of E / groups (1 <= groups <= 64,
  *                dividing E).  A group's value is the sum of its two largest c (of its only
  *                one where just one can be chosen) with a bias, its largest logit without.
- *                Experts are chosen from the topk_groups groups of largest value only
- *                (1 <= topk_groups <= groups, topk <= topk_groups * E / groups)
+ *                (A sum in FP32: -inf, the least, where it is below that range.  A group with
+ *                nothing to choose comes after all others.)  Experts are chosen from the
+ *                topk_groups groups of largest value only (1 <= topk_groups <= groups,
+ *                topk <= topk_groups * E / groups)
  *   topk_idx[t]  the experts of the topk largest c (logits), largest first; equal values,
  *                of groups too: the lowest id.  A logit or a c of -inf or NaN is never
  *                chosen; a token is live if it is not masked and has an expert that can be.

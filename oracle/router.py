@@ -41,7 +41,8 @@ def choose(z, k, score=SOFTMAX, bias=None, groups=1, topk_groups=1, mask=None):
             with np.errstate(all="ignore"):
                 both = value.astype(np.float32) + second.astype(np.float32)
             value = np.where(second > -np.inf, both, value)
-        best = np.argsort(-value, axis=1, kind="stable")[:, :topk_groups]
+        # (a group with nothing to choose after one whose sum of two is -inf)
+        best = np.lexsort((-value, part[:, :, 0] == -np.inf), axis=1)[:, :topk_groups]
         shut = np.ones((T, groups), bool)
         np.put_along_axis(shut, best, False, 1)
         c = np.where(np.repeat(shut, E // groups, 1), -np.inf, c)

@@ -27,8 +27,8 @@ __all__ = [
     "PROBE_COPY", "PROBE_READ", "PROBE_FILL", "PROBE_STRIDED_READ", "PROBE_STRIDED_WRITE",
     "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm", "mxfp4_grouped_gemm", "mxfp4_gemm_tiled",
     "moe_router", "moe_router_backward", "moe_router_workspace_size", "ROUTER_SOFTMAX", "ROUTER_SIGMOID",
-    "moe_bias_update", "rmsnorm_quant", "rmsnorm_backward", "rmsnorm_backward_workspace_size",
-    "grad_sumsq", "grad_clip", "grad_sumsq_workspace_size",
+    "moe_router_grouped_workspace_size", "moe_bias_update", "rmsnorm_quant", "rmsnorm_backward",
+    "rmsnorm_backward_workspace_size", "grad_sumsq", "grad_clip", "grad_sumsq_workspace_size",
     "E4M3", "E5M2", "E2M1", "SCALE_CEIL", "SCALE_OCP_FLOOR", "F32", "BF16", "ROW1x128", "ROW1x32", "BLOCK128", "GEMM_EXACT", "GEMM_FAST",
 ]
 
@@ -54,8 +54,8 @@ SYMBOLS = [
     "fp8_block_gemm_fmt", "fp8_grouped_gemm_masked", "fp8_quant_blockwise_t", "swiglu_f32", "dswiglu_f32",
     "permute_pad_noalloc", "fgb_hbm_probe", "mxfp4_quant", "mxfp4_quant_t", "mxfp4_dequant", "mxfp4_gemm",
     "mxfp4_grouped_gemm", "mxfp4_gemm_tiled", "moe_router", "moe_router_workspace_size", "moe_router_backward",
-    "moe_router_grouped", "moe_bias_update", "rmsnorm_quant", "rmsnorm_backward", "rmsnorm_backward_workspace_size",
-    "grad_sumsq", "grad_sumsq_workspace_size", "grad_clip",
+    "moe_router_grouped", "moe_router_grouped_workspace_size", "moe_bias_update", "rmsnorm_quant", "rmsnorm_backward",
+    "rmsnorm_backward_workspace_size", "grad_sumsq", "grad_sumsq_workspace_size", "grad_clip",
 ]
 
 
@@ -127,6 +127,7 @@ _SIG = {
                                    _p]),
     "moe_router_grouped": (_i32, [_p, _i32, _i64, _i32, _i64, _i32, _p, _p, _i32, _i32, _i32, _i32, _f32, _f32, _p, _p,
                                   _p, _p, _p, _sz, _p]),
+    "moe_router_grouped_workspace_size": (_sz, [_i64, _i32]),
     "moe_bias_update": (_i32, [_p, _p, _i32, _f32, _p, _p]),
     "rmsnorm_quant": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _p, _i32, _f32, _i32, _p, _i64, _p, _p, _p, _p,
                              _i32, _i64, _p]),
@@ -1094,6 +1095,12 @@ def moe_router_workspace_size(T, E):
     return int(_lib.moe_router_workspace_size(T, E))
 
 
+def moe_router_grouped_workspace_size(T, E):
+    """Bytes for moe_router with a bias or groups (moe_router_workspace_size's are enough, but slower up to 4096
+    tokens)."""
+    return int(_lib.moe_router_grouped_workspace_size(T, E))
+
+
 def _router_logits(logits, topk, name):
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError(f"{name}: logits must be [T, E] with unit column stride")
@@ -1130,7 +1137,9 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
         if not 1 <= topk_groups <= groups or topk > topk_groups * (E // groups):
             raise ValueError(f"{name}: topk_groups must be in [1, groups] and hold topk experts, got {topk_groups}")
     dev = _check_dev(logits, token_mask, workspace, bias)
-    need = 0 if workspace is not None else _lib.moe_router_workspace_size(T, E)
+    plain = bias is None and groups == 1
+    need = 0 if workspace is not None else (_lib.moe_router_workspace_size if plain else
+                                            _lib.moe_router_grouped_workspace_size)(T, E)
     idx, weights, counts, *more = _tensors.empties(
         logits, (_KI32, T, topk), (F32, T, topk), (_KI32, E + 1), *(((_KU8, need),) if need else ()),
         *(((F32,),) if loss_coef else ()))
@@ -1139,7 +1148,7 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
     loss = more[-1] if loss_coef else None
     out = (score, int(bool(renorm)), scale, loss_coef, _ptr(idx), _ptr(weights), _ptr(counts), _ptr(loss),
            _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(logits))
-    if bias is None and groups == 1:
+    if plain:
         _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), *out)
     else:
         _call_on(dev, "moe_router_grouped", _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), _ptr(bias),

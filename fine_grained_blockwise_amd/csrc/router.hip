@@ -472,7 +472,7 @@ int router_forward_args(const char *name, RouterArgs &a, int64_t blocks, const v
     FGB_REQUIRE(counts && (T == 0 || (topk_idx && weights)), FGB_EINVAL, "%s: null pointer", name);
     FGB_REQUIRE((((uintptr_t)topk_idx | (uintptr_t)weights | (uintptr_t)counts | (uintptr_t)loss) & 3) == 0, FGB_EINVAL,
                 "%s: outputs must be 4-byte aligned", name);
-    const size_t need = moe_router_workspace_size(T, E);
+    const size_t need = router_workspace(blocks, E);
     FGB_REQUIRE(need == 0 || (workspace && ws_bytes >= need), FGB_EWORKSPACE, "%s: workspace of %zu bytes needed", name,
                 need);
     FGB_REQUIRE(((uintptr_t)workspace & 7) == 0, FGB_EINVAL, "%s: workspace must be 8-byte aligned", name);
@@ -509,9 +509,7 @@ extern "C" size_t moe_router_workspace_size(int64_t T, int E)
 {
     if (T < 0 || E < 1 || E > 1024)
         return 0;
-    const int64_t plain = router_blocks(T, router_lanes(E)), grouped = router_blocks(T, grouped_lanes(T, E));
-    const int64_t blocks = plain > grouped ? plain : grouped;
-    return blocks == 1 ? 0 : (size_t)(reduce_blocks(E) + 1) * 8 + (size_t)blocks * (2 * (size_t)E + 1) * 4;
+    return router_workspace(router_blocks(T, router_lanes(E)), E);
 }
 
 extern "C" int moe_router(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk,

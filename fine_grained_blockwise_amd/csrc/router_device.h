@@ -326,6 +326,11 @@ static int grouped_lanes(int64_t T, int E)
 }
 
 static int reduce_blocks(int E) { return E <= 32 ? 1 : (E + 15) / 16; }
+// Bytes of workspace for the partial results of that many workgroups.
+static size_t router_workspace(int64_t blocks, int E)
+{
+    return blocks == 1 ? 0 : (size_t)(reduce_blocks(E) + 1) * 8 + (size_t)blocks * (2 * (size_t)E + 1) * 4;
+}
 
 // What both entry points of the forward pass check, and their arguments (router.hip).
 int check_router(const char *name, const void *z, int dtype, int64_t T, int E, int64_t ldz, int k, int score);

@@ -686,7 +686,7 @@ int mxfp4_gemm_tiled(int a_fmt, int64_t M, int64_t N, int64_t K, int G);
  *   A NaN logit of a live token (with softmax scores +inf too) makes NaN of what sums
  *   over it: the loss, softmax and renormed weights, and the token's gradient.
  *   workspace: moe_router_workspace_size(T, E) bytes (0 for a few tokens, then it may
- *   be NULL), contents on entry irrelevant.
+ *   be NULL; never fewer for more tokens), contents on entry irrelevant.
  * Sums are fp32 in a fixed order: results are the same on every run.
  */
 int moe_router(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk, const uint8_t *token_mask,
@@ -721,13 +721,16 @@ int moe_router_backward(const void *logits, int dtype, int64_t T, int E, int64_t
  *   topk_idx[t]  the experts of the topk largest c (logits), largest first; equal values,
  *                of groups too: the lowest id.  A logit or a c of -inf or NaN is never
  *                chosen; a token is live if it is not masked and has an expert that can be.
- * Other arguments, and the workspace, as for moe_router.  moe_router_backward gives the
- * gradient: the choice, and with it the bias, are constants of it.
+ * Other arguments as for moe_router.  workspace: moe_router_grouped_workspace_size(T, E) bytes
+ * (never fewer for more tokens).  moe_router's is enough, but then fewer workgroups share up
+ * to 4096 tokens, and the loss's low bits are those of their order.  moe_router_backward gives
+ * the gradient: the choice, and with it the bias, are constants of it.
  */
 int moe_router_grouped(const void *logits, int dtype, int64_t T, int E, int64_t ld, int topk, const uint8_t *token_mask,
                        const float *bias, int groups, int topk_groups, int score, int renorm, float scale,
                        float loss_coef, int32_t *topk_idx, float *weights, int32_t *counts, float *loss,
                        void *workspace, size_t ws_bytes, void *stream);
+size_t moe_router_grouped_workspace_size(int64_t T, int E);
 
 /*
  * moe_bias_update -- the bias for the next step: out[e] = bias[e] + rate where counts[e] is

@@ -1,7 +1,8 @@
 // grads.hip -- the global norm of many gradients, and their clipping.
 //
 //   S = sum over all tensors of g^2, norm = scale sqrt(S),
-//   out = g scale min(1, max_norm / norm); a norm that is infinite or NaN clips nothing.
+//   out = g scale min(1, max_norm / norm); a norm that is infinite or NaN in FP32, as it is
+//   returned, clips nothing.
 //
 // Squares and sums are FP64: the square of a BF16 or FP32 value is exact and neither over- nor
 // underflows.  Every sum has a fixed order: a thread's values, the workgroup's threads, the
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(GradList l, const doubl
     if (parts > 0) // uniform
         sum = block_sum<256>((int)threadIdx.x < parts ? squares[threadIdx.x] : 0.0);
     const double norm = scale * sqrt(sum);
-    const bool clip = norm > max_norm && norm < __builtin_inf();
+    const bool clip = norm > max_norm && (float)norm < __builtin_inff();
     const float f = (float)(clip ? scale * (max_norm / norm) : scale);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0)
         *norm_out = (float)norm;

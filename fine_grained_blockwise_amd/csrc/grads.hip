@@ -196,18 +196,28 @@ __global__ __launch_bounds__(1024) void grad_total_kernel(const double *part, in
         *out = accumulate ? *out + sum : sum;
 }
 
-template <bool IN, bool OUT>
-__device__ __forceinline__ void piece_scale(const void *p, void *o, int64_t from, int n, float f)
+template <bool IN, bool OUT, class Times> __device__ __forceinline__ void piece_scale(const Piece &k, Times times)
 {
     over_piece<IN>(
-        p, from, n,
+        k.p, k.from, k.n,
         [&](int64_t at, float (&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                v[j] *= f;
-            store8g<OUT>(o, at, v);
+                v[j] = times(v[j]);
+            store8g<OUT>(k.o, at, v);
         },
-        [&](int64_t at, float v) { store1g<OUT>(o, at, v * f); });
+        [&](int64_t at, float v) { store1g<OUT>(k.o, at, times(v)); });
+}
+template <class Times> __device__ __forceinline__ void scale_kind(const Piece &k, Times times)
+{
+    if (k.kind == 3)
+        piece_scale<true, true>(k, times);
+    else if (k.kind == 2)
+        piece_scale<false, true>(k, times);
+    else if (k.kind == 1)
+        piece_scale<true, false>(k, times);
+    else
+        piece_scale<false, false>(k, times);
 }
 
 // squares: the sum (parts = 0), or up to FEW_PARTS parts of it, which every workgroup adds
@@ -222,7 +232,9 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(GradList l, const doubl
         sum = block_sum<256>((int)threadIdx.x < parts ? squares[threadIdx.x] : 0.0);
     const double norm = scale * sqrt(sum);
     const bool clip = norm > max_norm && (float)norm < __builtin_inff();
-    const float f = (float)(clip ? scale * (max_norm / norm) : scale);
+    const double factor = clip ? scale * (max_norm / norm) : scale;
+    const float f = (float)factor;
+    const bool beyond = factor < 0x1p-126 || factor > 0x1.fffffep127; // FP32 holds fewer than 24 bits of it
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0)
         *norm_out = (float)norm;
     if (l.count == 0)
@@ -233,14 +245,10 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(GradList l, const doubl
         const Piece k = ends.piece(l, chunks - 1 - c);
         if (f == 1.0f && k.p == k.o)
             continue; // in place and unchanged
-        if (k.kind == 3)
-            piece_scale<true, true>(k.p, k.o, k.from, k.n, f);
-        else if (k.kind == 2)
-            piece_scale<false, true>(k.p, k.o, k.from, k.n, f);
-        else if (k.kind == 1)
-            piece_scale<true, false>(k.p, k.o, k.from, k.n, f);
+        if (beyond) // uniform
+            scale_kind(k, [&](float v) { return (float)(v * factor); });
         else
-            piece_scale<false, false>(k.p, k.o, k.from, k.n, f);
+            scale_kind(k, [&](float v) { return v * f; });
     }
 }
 

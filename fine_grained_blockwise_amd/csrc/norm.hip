@@ -247,7 +247,7 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_grad_kernel(NormGradA
         for (int i = 0; i < 8; i++) {
             dw[u][i] = 0.0f;
             if constexpr (!AGAIN)
-                w[u][i] = 0.0f; // (columns past the last one add nothing)
+                w[u][i] = 0.0f; // (columns past the last one: not stored, not summed)
         }
         if constexpr (!AGAIN)
             if (c < a.cols)
@@ -307,6 +307,7 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_grad_kernel(NormGradA
                 widen<HBF>(rh[u], h[u]);
                 if (a.dh)
                     widen<HBF>(re[u], e[u]);
+                const float before = sum;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     h[u][i] *= rstd;
@@ -316,6 +317,8 @@ __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_grad_kernel(NormGradA
                     if (!a.dh)
                         e[u][i] = 0.0f;
                 }
+                // (a weight of 0 does not keep out the infinities of columns that are loaded once more)
+                sum = chunk_col<W>(u, t) < a.cols ? sum : before;
             }
             const float mean = row_sum<W>(sum, red[odd]) / (float)a.cols;
             odd ^= 1;

@@ -246,7 +246,7 @@ __device__ __forceinline__ void router_bwd_far(const RouterArgs &a, float *part,
         m = SCORE == FGB_ROUTER_SIGMOID ? fminf(m, 0.0f) : m;
         const float zr = on ? logit(slot) : NEG_INF;
         const float total = group_sum<L>(on ? numerator<SCORE>(zr, m) : 0.0f);
-        const bool live = group_max<L>(on) != 0, far = live && total < 2.0f * FAR;
+        const bool live = group_max<L>(slot >= 0 ? 1u : 0u) != 0, far = live && total < 2.0f * FAR; // as that pass has it
         if (!__any(far))
             continue;
         // the slots' parts, to their experts

@@ -698,7 +698,7 @@ size_t moe_router_workspace_size(int64_t T, int E);
  * moe_router_backward -- the gradient of the logits from dweights [T, topk]
  * (NULL: zeros) and dloss (device scalar, NULL: 0): scores are recomputed from
  * the logits, topk_idx and counts are the forward's (counts are constants of the
- * loss, as usual for this loss).  Gradients of slots with id -1 are ignored;
+ * loss, as usual for this loss).  Gradients of slots with an id outside [0, E) are ignored;
  * tokens that were not live get zeros.  dlogits [T, E], row stride ldd, in the
  * logits' type (BF16: nearest even).  Other arguments as in the forward call.
  */

@@ -1265,6 +1265,7 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
         raise ValueError(f"{name}: eps must be positive")
     if h is not None and residual is None:
         raise ValueError(f"{name}: h needs a residual")
+    stream = x  # (a copy with aligned rows may take x's place below)
     usual = _tensors.usual(x, weight, residual)
     if usual is not None:
         rows, cols, x_at, x_code, w_at, w_code, r_at, r_code = usual
@@ -1302,7 +1303,7 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
             q, s = _tensors.empties(x, (_KU8, rows, cols), (_KU8, rows, cols // group))
     _call_on(dev, name, x_at, x_code, rows, cols, ldx, r_at, r_code, ldr, w_at, w_code, eps, group, _ptr(h), ldh,
              rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype], cols, _stream(x))
-    return q, s, y, x if h is None else h, rstd
+    return q, s, y, stream if h is None else h, rstd
 
 
 def rmsnorm_backward_workspace_size(rows, cols):

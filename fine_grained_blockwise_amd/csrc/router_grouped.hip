@@ -363,6 +363,7 @@ __global__ __launch_bounds__(1024) void moe_bias_kernel(const float *b, const in
 {
     __shared__ long long red[16];
     const int e = threadIdx.x;
+    const float before = e < E ? b[e] : 0.0f; // (all of it before anything is written: out may lie over it)
     long long c = e < E ? counts[e] : 0, sum = c;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1)
@@ -375,7 +376,7 @@ __global__ __launch_bounds__(1024) void moe_bias_kernel(const float *b, const in
         sum += red[i];
     c *= E;
     if (e < E)
-        out[e] = b[e] + (c < sum ? rate : c > sum ? -rate : 0.0f);
+        out[e] = before + (c < sum ? rate : c > sum ? -rate : 0.0f);
 }
 
 } // namespace fgb

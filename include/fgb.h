@@ -734,7 +734,7 @@ size_t moe_router_grouped_workspace_size(int64_t T, int E);
 
 /*
  * moe_bias_update -- the bias for the next step: out[e] = bias[e] + rate where counts[e] is
- * below the mean of counts[0 .. E), - rate above it, bias[e] at it.  out may be bias.
+ * below the mean of counts[0 .. E), - rate above it, bias[e] at it.  out may lie over bias.
  */
 int moe_bias_update(const float *bias, const int32_t *counts, int E, float rate, float *out, void *stream);
 

@@ -1255,7 +1255,7 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
 
     h is the sum in the residual's type (x itself without a residual), y = h * rstd * weight in y_dtype (None: not
     written), q and s the codes and scales of y before its rounding (None with quant=False).  h= takes a tensor for
-    the sum; it may be the residual itself."""
+    the sum; it may be the residual itself or, of the same type, x, and lie over nothing else."""
     name = "rmsnorm_quant"
     if group not in (32, 128):
         raise ValueError(f"{name}: group must be 32 or 128, got {group}")
@@ -1315,7 +1315,8 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
     dweight fp32 [cols]).
 
     dx is the gradient of h, and so of x and the residual, with dh (what reaches h past the norm, in h's dtype) added
-    before its rounding; dx= takes a tensor for it, which may be dh or dy itself."""
+    before its rounding; dx= takes a tensor for it, which may be dh, h or dy itself and lie over nothing
+    else."""
     name = "rmsnorm_backward"
     usual = _tensors.usual(dy, weight, h, dh)
     if usual is not None:

@@ -395,6 +395,63 @@ static int check_rows(const char *name, const char *what, const void *p, int dty
     return FGB_OK;
 }
 
+// Rows in memory that a call reads or writes: `rows` of them of `bytes`, `ld` bytes apart.
+struct Rows {
+    const char *name;
+    uintptr_t p;
+    int64_t rows, bytes, ld;
+};
+static Rows rows_at(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int dtype)
+{
+    const int each = dtype == FGB_BF16 ? 2 : 4;
+    return {name, (uintptr_t)p, p ? rows : 0, cols * each, ld * each};
+}
+static Rows bytes_at(const char *name, const void *p, int64_t bytes) { return {name, (uintptr_t)p, p ? 1 : 0, bytes, bytes}; }
+
+// Whether two of them share a byte.  Views of one buffer (one row stride) are compared at once,
+// as rows i of a and j of b meet or not by i - j alone; others a row of the shorter at a time.
+static bool share(const Rows &a, const Rows &b)
+{
+    if (a.rows > b.rows)
+        return share(b, a);
+    if (a.rows < 1 || a.bytes < 1 || b.bytes < 1)
+        return false;
+    const int64_t lda = a.rows == 1 ? b.ld : a.ld, to = (int64_t)(b.p - a.p); // (b.p from a.p)
+    if (to >= (a.rows - 1) * lda + a.bytes || to + (b.rows - 1) * b.ld + b.bytes <= 0)
+        return false;
+    // the first row of b that ends behind row i of a
+    const auto meets = [&](int64_t i) {
+        const int64_t past = i * lda - to - b.bytes, j = past < 0 ? 0 : past / b.ld + 1;
+        return j < b.rows && to + j * b.ld < i * lda + a.bytes;
+    };
+    if (lda == b.ld && a.bytes <= lda) {
+        // with i - j = m: m ld < to + b.bytes and m ld + a.bytes > to
+        const int64_t q = to / b.ld;
+        for (int64_t m = q - 2; m <= q + 2; m++)
+            if (m > -b.rows && m < a.rows && m * b.ld < to + b.bytes && m * b.ld + a.bytes > to)
+                return true;
+        return false;
+    }
+    for (int64_t i = 0; i < a.rows; i++)
+        if (meets(i))
+            return true;
+    return false;
+}
+// The very same rows: what an output may be of an input, as a row is written after it was read.
+static bool same(const Rows &a, const Rows &b)
+{
+    return a.p == b.p && a.bytes == b.bytes && (a.ld == b.ld || a.rows == 1);
+}
+static int check_apart(const char *name, const Rows &out, const Rows &other)
+{
+    FGB_REQUIRE(!share(out, other), FGB_EINVAL, "%s: %s lies over %s", name, out.name, other.name);
+    return FGB_OK;
+}
+static int check_apart_or_same(const char *name, const Rows &out, const Rows &in)
+{
+    return same(out, in) ? FGB_OK : check_apart(name, out, in);
+}
+
 // The variant by the columns: waves a row and chunks a lane.
 #define FGB_NORM_VARIANT(COLS, LAUNCH)                                                                                 \
     do {                                                                                                               \
@@ -466,6 +523,20 @@ extern "C" int rmsnorm_quant(const void *x, int x_dtype, int64_t rows, int64_t c
     if (y && (rc = check_rows(name, "y", y, y_dtype, cols, ldy)) != FGB_OK)
         return rc;
     FGB_REQUIRE(aligned16(q), FGB_EINVAL, "%s: q must be 16-byte aligned", name);
+    const Rows ins[] = {rows_at("x", x, rows, cols, ldx, x_dtype), rows_at("residual", residual, rows, cols, ldr, r_dtype)};
+    const Rows outs[] = {rows_at("h", residual ? h : nullptr, rows, cols, ldh, r_dtype), rows_at("y", y, rows, cols, ldy, y_dtype),
+                         bytes_at("q", q, rows * cols), bytes_at("s", s, rows * (cols / group)), bytes_at("rstd", rstd, 4 * rows)};
+    const Rows w_rows = rows_at("weight", weight, 1, cols, cols, w_dtype);
+    for (int i = 0; i < 5; i++) {
+        for (const Rows &in : ins)
+            if ((rc = i < 2 ? check_apart_or_same(name, outs[i], in) : check_apart(name, outs[i], in)) != FGB_OK)
+                return rc;
+        if ((rc = check_apart(name, outs[i], w_rows)) != FGB_OK)
+            return rc;
+        for (int j = 0; j < i; j++)
+            if ((rc = check_apart(name, outs[i], outs[j])) != FGB_OK)
+                return rc;
+    }
     FGB_REQUIRE(rstd && ((uintptr_t)rstd & 3) == 0, FGB_EINVAL, "%s: rstd null or misaligned", name);
     NormArgs a{};
     a.x = x; a.r = residual; a.w = weight; a.h = h; a.y = y; a.q = q; a.s = s; a.rstd = rstd;
@@ -513,6 +584,19 @@ extern "C" int rmsnorm_backward(const void *dy, int dy_dtype, int64_t rows, int6
                 FGB_EINVAL, "%s: dweight or rstd null or misaligned", name);
     const size_t need = rmsnorm_backward_workspace_size(rows, cols);
     FGB_REQUIRE(workspace && ws_bytes >= need, FGB_EWORKSPACE, "%s: workspace of %zu bytes needed", name, need);
+    const Rows dx_rows = rows_at("dx", dx, rows, cols, lddx, h_dtype), w_rows = rows_at("weight", weight, 1, cols, cols, w_dtype);
+    const Rows part = bytes_at("workspace", workspace, (int64_t)need), scale = bytes_at("rstd", rstd, 4 * rows);
+    const Rows sum = bytes_at("dweight", dweight, 4 * cols);
+    const Rows ins[] = {rows_at("dy", dy, rows, cols, lddy, dy_dtype), rows_at("h", h, rows, cols, ldh, h_dtype),
+                        rows_at("dh", dh, rows, cols, lddh, h_dtype)};
+    for (const Rows &in : ins)
+        if ((rc = check_apart_or_same(name, dx_rows, in)) != FGB_OK || (rc = check_apart(name, part, in)) != FGB_OK)
+            return rc;
+    for (const Rows *other : {&w_rows, &scale, &sum})
+        if ((rc = check_apart(name, dx_rows, *other)) != FGB_OK || (rc = check_apart(name, part, *other)) != FGB_OK)
+            return rc;
+    if ((rc = check_apart(name, part, dx_rows)) != FGB_OK)
+        return rc;
     FGB_REQUIRE(aligned16(workspace), FGB_EINVAL, "%s: workspace must be 16-byte aligned", name);
     NormGradArgs a{};
     a.dy = dy; a.h = h; a.w = weight; a.dh = dh; a.rstd = rstd; a.dx = dx;

@@ -747,12 +747,13 @@ int moe_bias_update(const float *bias, const int32_t *counts, int E, float rate,
  *   residual [rows, cols], row stride ldr, either type; NULL: none (h, ldh are then unused)
  *   weight   [cols], either type; eps > 0; group 128 or 32
  *   h        [rows, cols], row stride ldh, in the residual's type: the new residual stream.
- *            It may be the residual itself (or, of the same type, x); no other overlap
+ *            It may be the residual itself (or, of the same type, x)
  *   rstd     [rows] FP32, for rmsnorm_backward
  *   q, s     [rows, cols] codes and [rows, cols / group] scales, dense (cols % group == 0), of
  *            the FP32 y as fp8_quant_rowwise gives them; both NULL: not wanted
  *   y        [rows, cols], row stride ldy, y in y_dtype (BF16: nearest even); NULL: not wanted.
- *            (Codes or y have to be.)
+ *            (Codes or y have to be.)  It may be x or the residual itself, of the same type
+ * An output that lies over anything else of the call is refused.
  * The sum of squares is FP32: it has to be in that range.
  */
 int rmsnorm_quant(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void *residual,
@@ -767,7 +768,8 @@ int rmsnorm_quant(const void *x, int x_dtype, int64_t rows, int64_t cols, int64_
  *   dweight = sum over the rows of dy * hat; [cols] FP32
  *   dy  [rows, cols], row stride lddy, either type; h, rstd: the forward's (x, without a
  *       residual); dh [rows, cols], row stride lddh, in h's type: the gradient that reaches h
- *       past the norm; NULL: 0.  dx may be dy (of the same type) or dh itself
+ *       past the norm; NULL: 0.  dx may be dy (of the same type), h or dh itself; lying
+ *       over anything else of the call is refused, as it is of the workspace
  *   workspace: rmsnorm_backward_workspace_size(rows, cols) bytes, contents on entry irrelevant.
  * rows = 0 gives a dweight of zeros.
  */

@@ -296,16 +296,15 @@ static int check_grads(const char *name, int n, const void *const *grads, const 
 }
 
 // No output may lie over another one, or over a gradient that is not its own.
-static bool outputs_overlap(int n, const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
-                            const int *out_dtypes)
+static int check_outputs(int n, const void *const *grads, void *const *outs, const int64_t *numel, const int *dtypes,
+                         const int *out_dtypes)
 {
     struct Span {
         uintptr_t from, to;
         int of, out;
     };
     Span *const spans = new (std::nothrow) Span[2 * (size_t)n];
-    if (!spans)
-        return true;
+    FGB_REQUIRE(spans, FGB_ENOMEM, "grad_clip: no host memory to compare the places of %d tensors", n);
     int m = 0;
     for (int i = 0; i < n; i++) {
         if (numel[i] == 0)
@@ -325,7 +324,8 @@ static bool outputs_overlap(int n, const void *const *grads, void *const *outs, 
             out_end = std::max(out_end, spans[i].to);
     }
     delete[] spans;
-    return bad;
+    FGB_REQUIRE(!bad, FGB_EINVAL, "grad_clip: an output lies over another one or over a gradient that is not its own");
+    return FGB_OK;
 }
 
 // Partial sums of all launches of a list: its non-empty tensors in runs of LIST.
@@ -413,8 +413,8 @@ extern "C" int grad_clip(const void *const *grads, void *const *outs, const int6
     }
     FGB_REQUIRE(max_norm > 0.0 && scale > 0.0 && scale < __builtin_inf(), FGB_EINVAL,
                 "grad_clip: max_norm and scale must be positive");
-    FGB_REQUIRE(!outputs_overlap(n, grads, outs, numel, dtypes, out_dtypes), FGB_EINVAL,
-                "grad_clip: an output lies over another one or over a gradient that is not its own");
+    if ((rc = check_outputs(n, grads, outs, numel, dtypes, out_dtypes)) != FGB_OK)
+        return rc;
     FGB_REQUIRE(((uintptr_t)sumsq & 7) == 0 && norm && ((uintptr_t)norm & 3) == 0, FGB_EINVAL,
                 "grad_clip: sumsq misaligned, or norm null or misaligned");
     const hipStream_t st = (hipStream_t)stream;

@@ -50,6 +50,7 @@ extern "C" {
 #define FGB_EUNSUPPORTED 2 /* dtype / granularity combination not provided */
 #define FGB_EWORKSPACE 3   /* workspace missing or too small */
 #define FGB_EHIP 4         /* a HIP runtime call failed (launch error) */
+#define FGB_ENOMEM 5       /* no host memory for the call's own lists */
 
 /* element types */
 #define FGB_F32 0

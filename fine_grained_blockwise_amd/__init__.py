@@ -5,8 +5,9 @@ only marshals arguments: it checks shapes, allocates outputs with
 ``torch.empty`` on the input's device and calls the C entry point of the same
 name on torch's current HIP stream.  All arithmetic runs in the HIP kernels.
 
-There is no fallback: if libfgb.so (or _tensors.so, which looks through lists
-of tensors) is missing, importing this package raises.
+There is no fallback: if libfgb.so is missing, or _tensors (which looks through
+lists of tensors) is or was built against another torch, importing this package
+raises.
 """
 import ctypes as C
 import os
@@ -65,11 +66,18 @@ class FgbError(RuntimeError):
         self.code = code
 
 
+_REBUILD = "build it with `python -c 'import __graft_entry__ as g; g.build()'`"
 if not os.path.exists(LIB_PATH):
-    raise ImportError(f"libfgb.so not found at {LIB_PATH}; build it with "
-                      "`python -c 'import __graft_entry__ as g; g.build()'`")
+    raise ImportError(f"libfgb.so not found at {LIB_PATH}; {_REBUILD}")
 
-from . import _tensors  # noqa: E402  (needs torch's libraries, loaded above)
+try:
+    from . import _tensors  # (needs torch's libraries, loaded above)
+except ImportError as _e:
+    raise ImportError(f"the extension module _tensors is missing, or was built against another Python or torch than "
+                      f"this one ({torch.__version__}): {_e}; {_REBUILD}") from _e
+if getattr(_tensors, "torch_version", None) != str(torch.__version__):
+    raise ImportError(f"the extension module _tensors was built against torch "
+                      f"{getattr(_tensors, 'torch_version', '(unknown)')}, this is {torch.__version__}; {_REBUILD}")
 
 _lib = C.CDLL(LIB_PATH)
 _p, _i64, _i32, _sz, _f32, _f64 = C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_float, C.c_double

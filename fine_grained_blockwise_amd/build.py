@@ -3,13 +3,15 @@
 Every .hip file under csrc/ is compiled with hipcc to an object, then linked
 into fine_grained_blockwise_amd/libfgb.so.  Packed-FP32 VALU ops are disabled
 and floating-point contraction is off, so every fp32 operation rounds where
-the source says it does.  Beside it _tensors.so, the binding's helper for lists
-of tensors, is compiled against the installed torch (host code only).
+the source says it does.  Beside it _tensors, the binding's extension module for
+lists of tensors, is compiled against the installed torch and Python, whose
+versions it carries (host code only).
 """
 import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import runpy
 import subprocess
 import sysconfig
 
@@ -17,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfgb.so")
-TENSORS = os.path.join(HERE, "_tensors.so")
+TENSORS = os.path.join(HERE, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))  # (another Python does not see it)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -44,8 +46,9 @@ def _compile(src):
 
 def _build_tensors():
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    version = runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
     tmp = TENSORS + ".tmp"
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", os.path.join(torch, "include"),
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f'-DFGB_TORCH="{version}"', "-I", os.path.join(torch, "include"),
            "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "tensor_list.cpp"),
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-o", tmp]
@@ -56,7 +59,7 @@ def _build_tensors():
 
 
 def build(jobs=8, verbose=False):
-    """Compile every HIP source and link libfgb.so, and _tensors.so; returns the library path."""
+    """Compile every HIP source and link libfgb.so, and _tensors; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(jobs, len(srcs) + 1)) as ex:

@@ -14,6 +14,9 @@
 // None) where all are as the calls mostly have them: FP32 or BF16, on one GPU, contiguous and
 // 16-byte aligned, the matrices of one shape [rows, cols], the vector [cols].  None where
 // anything is not: the caller then looks for what it is.  (3 us in Python, 0.3 us here.)
+//
+// torch_version: that of the torch which this was compiled against.  Another's tensors may be laid
+// out differently, so the package does not go on with it.
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -147,4 +150,12 @@ static PyMethodDef methods[] = {
     {nullptr, nullptr, 0, nullptr}};
 static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
-PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensors(void)
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", FGB_TORCH) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -162,6 +162,9 @@ def symbols():
 
 
 def _call(name, *args):
+    """The C entry point `name`; args end with _stream()'s handle, whose device it runs on."""
+    if type(args[-1]) is not int:
+        return _call_on(args[-1].device, name, *args[:-1], int(args[-1]))
     rc = getattr(_lib, name)(*args)
     if rc != 0:
         raise FgbError(name, rc, _lib.fgb_last_error().decode())
@@ -191,13 +194,22 @@ def _ptr(t):
 
 # The handle of torch's current stream, without building a Stream object for it
 # (2 us a call, as much as half a launch).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _StreamOf(int):
+    """A stream's handle on a device that is not the current one."""
 
 
 def _stream(t):
-    if _raw_stream is not None:
-        return _raw_stream(t.device.index)
-    return torch.cuda.current_stream(t.device).cuda_stream
+    """torch's current stream on t's device: an int, or _StreamOf, which _call makes its device current for."""
+    index = t.get_device()
+    handle = _raw_stream(index)
+    if index != _current_device():
+        handle = _StreamOf(handle)
+        handle.device = t.device
+    return handle
 
 
 def _dtype_code(t):
@@ -1144,7 +1156,7 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
             raise ValueError(f"{name}: groups must be in [1, 64] and divide E ({E}), got {groups}")
         if not 1 <= topk_groups <= groups or topk > topk_groups * (E // groups):
             raise ValueError(f"{name}: topk_groups must be in [1, groups] and hold topk experts, got {topk_groups}")
-    dev = _check_dev(logits, token_mask, workspace, bias)
+    _check_dev(logits, token_mask, workspace, bias)
     plain = bias is None and groups == 1
     need = 0 if workspace is not None else (_lib.moe_router_workspace_size if plain else
                                             _lib.moe_router_grouped_workspace_size)(T, E)
@@ -1159,8 +1171,8 @@ def moe_router(logits, topk, score=ROUTER_SOFTMAX, renorm=False, scale=1.0, loss
     if plain:
         _call(name, _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), *out)
     else:
-        _call_on(dev, "moe_router_grouped", _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), _ptr(bias),
-                 groups, topk_groups, *out)
+        _call("moe_router_grouped", _ptr(logits), dt, T, E, _ld(logits), topk, _ptr(token_mask), _ptr(bias),
+              groups, topk_groups, *out)
     return idx, weights, counts, loss
 
 
@@ -1199,10 +1211,10 @@ def moe_bias_update(bias, counts, rate, out=None):
     _need(counts, f"{name}: counts", shape=(E + 1,), dtype=torch.int32, contiguous=True)
     if out is not None:
         _need(out, f"{name}: out", shape=(E,), dtype=torch.float32, contiguous=True)
-    dev = _check_dev(bias, counts, out)
+    _check_dev(bias, counts, out)
     if out is None:
         out, = _tensors.empties(bias, (F32, E))
-    _call_on(dev, name, bias.data_ptr(), counts.data_ptr(), E, rate, out.data_ptr(), _stream(bias))
+    _call(name, bias.data_ptr(), counts.data_ptr(), E, rate, out.data_ptr(), _stream(bias))
     return out
 
 
@@ -1291,7 +1303,7 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
             residual, r_code, ldr = _norm_rows(residual, f"{name}: residual", x.shape)
         _check_dev(x, weight, residual, h)
         x_at, w_at, r_at = x.data_ptr(), weight.data_ptr(), _ptr(residual)
-    dev, ldh = x.device, cols
+    ldh = cols
     if quant and cols % group:
         raise ValueError(f"{name}: cols ({cols}) must be a multiple of the group ({group})")
     if h is not None:
@@ -1309,8 +1321,8 @@ def rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=128, quant=True, y_d
             y, = _tensors.empties(x, (_CODES[_out_dtype(y_dtype, name)], rows, cols))
         if quant:
             q, s = _tensors.empties(x, (_KU8, rows, cols), (_KU8, rows, cols // group))
-    _call_on(dev, name, x_at, x_code, rows, cols, ldx, r_at, r_code, ldr, w_at, w_code, eps, group, _ptr(h), ldh,
-             rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype], cols, _stream(x))
+    _call(name, x_at, x_code, rows, cols, ldx, r_at, r_code, ldr, w_at, w_code, eps, group, _ptr(h), ldh,
+          rstd.data_ptr(), _ptr(q), _ptr(s), _ptr(y), F32 if y is None else _CODES[y_dtype], cols, _stream(x))
     return q, s, y, stream if h is None else h, rstd
 
 
@@ -1354,7 +1366,6 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
         _check_dev(dy, h, weight, rstd, dh, dx, workspace)
     else:
         _check_dev(dy, rstd)
-    dev = dy.device
     need = (_KU8, _lib.rmsnorm_backward_workspace_size(rows, cols))
     if dx is None and workspace is None:
         dx, workspace, dweight = _tensors.empties(dy, (h_code, rows, cols), need, (F32, cols))
@@ -1364,9 +1375,8 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, workspace=None):
             dx, = _tensors.empties(dy, (h_code, rows, cols))
         if workspace is None:
             workspace, = _tensors.empties(dy, need)
-    _call_on(dev, name, dy_at, dy_code, rows, cols, lddy, h_at, h_code, ldh, w_at, w_code, rstd.data_ptr(), dh_at, lddh,
-             dx.data_ptr(), lddx,
-             dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dy))
+    _call(name, dy_at, dy_code, rows, cols, lddy, h_at, h_code, ldh, w_at, w_code, rstd.data_ptr(), dh_at, lddh,
+          dx.data_ptr(), lddx, dweight.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dy))
     return dx, dweight
 
 
@@ -1414,8 +1424,8 @@ def grad_sumsq(grads, out=None, accumulate=False, workspace=None):
     _check_dev(grads[0], workspace)
     if out is None:
         out = torch.empty((), dtype=torch.float64, device=dev)
-    _call_on(dev, name, ptrs, numel, types, n, out.data_ptr(), 1 if accumulate else 0, workspace.data_ptr(),
-             workspace.numel(), _stream(out))
+    _call(name, ptrs, numel, types, n, out.data_ptr(), 1 if accumulate else 0, workspace.data_ptr(),
+          workspace.numel(), _stream(out))
     return out
 
 
@@ -1447,6 +1457,6 @@ def grad_clip(grads, max_norm, scale=1.0, out=None, sumsq=None, workspace=None):
         workspace = _grad_workspace(workspace, numel, n, dev, name)
         _check_dev(grads[0], workspace)
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    _call_on(dev, name, ptrs, optrs, numel, types, otypes, n, max_norm, scale, _ptr(sumsq), norm.data_ptr(),
-             _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(norm))
+    _call(name, ptrs, optrs, numel, types, otypes, n, max_norm, scale, _ptr(sumsq), norm.data_ptr(),
+          _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(norm))
     return norm

@@ -18,6 +18,7 @@
 // torch_version: that of the torch which this was compiled against.  Another's tensors may be laid
 // out differently, so the package does not go on with it.
 #include <ATen/ops/empty.h>
+#include <pybind11/pybind11.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
@@ -67,11 +68,13 @@ static PyObject *empties(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (n < 1 || !THPVariable_Check(args[0]))
         return PyErr_Format(PyExc_TypeError, "empties: expected a tensor first");
     const at::Device device = THPVariable_Unpack(args[0]).device();
-    THPObjectPtr out(PyTuple_New(n - 1));
-    if (!out)
-        return nullptr;
+    struct Spec {
+        int64_t v[4]; // the kind, then the sizes
+        size_t dims;
+    };
+    c10::SmallVector<Spec, 8> specs(n - 1);
     for (Py_ssize_t i = 1; i < n; i++) {
-        int64_t v[4];
+        int64_t *const v = specs[i - 1].v;
         const Py_ssize_t m = PyTuple_Check(args[i]) ? PyTuple_GET_SIZE(args[i]) : 0;
         if (m < 1 || m > 4)
             return PyErr_Format(PyExc_TypeError, "empties: expected (kind, up to three sizes)");
@@ -82,11 +85,23 @@ static PyObject *empties(PyObject *, PyObject *const *args, Py_ssize_t n)
         }
         if (v[0] > 3)
             return PyErr_Format(PyExc_ValueError, "empties: unknown kind");
-        PyObject *t = THPVariable_Wrap(at::empty(at::IntArrayRef(v + 1, (size_t)m - 1),
-                                                 at::TensorOptions().dtype(kinds[v[0]]).device(device)));
+        specs[i - 1].dims = (size_t)m - 1;
+    }
+    c10::SmallVector<at::Tensor, 8> tensors;
+    {
+        pybind11::gil_scoped_release others_run; // (the allocator may wait for the GPU)
+        for (const Spec &s : specs)
+            tensors.push_back(at::empty(at::IntArrayRef(s.v + 1, s.dims),
+                                        at::TensorOptions().dtype(kinds[s.v[0]]).device(device)));
+    }
+    THPObjectPtr out(PyTuple_New(n - 1));
+    if (!out)
+        return nullptr;
+    for (Py_ssize_t i = 0; i < n - 1; i++) {
+        PyObject *t = THPVariable_Wrap(std::move(tensors[i]));
         if (!t)
             return nullptr;
-        PyTuple_SET_ITEM(out.get(), i - 1, t);
+        PyTuple_SET_ITEM(out.get(), i, t);
     }
     return out.release();
     END_HANDLE_TH_ERRORS

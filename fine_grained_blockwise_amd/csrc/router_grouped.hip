@@ -40,11 +40,12 @@ __device__ __forceinline__ void lanes_two(int P, uint32_t &first, uint32_t &seco
 }
 
 // e^x, x in [-200, 200], to a relative 2^-50: x log2 e = n + r, |r| <= 1/2, and 2^r by its
-// Taylor polynomial (the first term left out is below 2^-52).
+// Taylor polynomial (the first term left out is below 2^-52).  log2 e is two numbers: one alone
+// is off by 2^-55.4, which x and ln 2 make 2^-48.2.
 __device__ __forceinline__ double exp64(double x)
 {
-    constexpr double LOG2E = 1.4426950408889634;
-    const double n = __builtin_rint(x * LOG2E), r = fma(x, LOG2E, -n);
+    constexpr double LOG2E = 1.4426950408889634, LOG2E_REST = 2.0355273740931033e-17;
+    const double n = __builtin_rint(x * LOG2E), r = fma(x, LOG2E_REST, fma(x, LOG2E, -n));
     // ln(2)^k / k!
     double p = 2.5678435993488205e-11;
     p = fma(p, r, 4.4455382718708116e-10);

@@ -13,9 +13,9 @@
 // groups' amax (16 or 4 neighbouring lanes) and the outputs all come from one read.
 // 8192 x 7168 BF16: forward 70 us (5.9 TB/s), gradient 78 us (6.0 TB/s) and 5 us for dw.
 //
-// Loads are streaming, stores ordinary: with streaming ones the gradient took 85 us, the
-// forward and a reader of its codes 103 (96 so).  A row's loads go out together, without
-// branches; waiting for each chunk in turn the gradient took 146 us.
+// BF16 loads are streaming (FP32 ones not: load8), stores ordinary: with streaming ones the
+// gradient took 85 us, the forward and a reader of its codes 103 (96 so).  A row's loads go out
+// together, without branches; waiting for each chunk in turn the gradient took 146 us.
 #include "fgb_internal.h"
 
 namespace fgb {
@@ -229,7 +229,8 @@ template <bool HBF> __device__ __forceinline__ void store_dx(const NormGradArgs 
 }
 
 // Sixteen waves have 128 registers a lane, which a row and its part of dw do not fit: they read
-// the row again after the sum (4096 x 32768: 286 us, from registers that spill 720).
+// the row again after the sum (4096 x 32768 BF16: 304 us under a trace, from registers that spill
+// 720).
 template <bool DBF, bool HBF, int W, int CH>
 __global__ __launch_bounds__(NORM_THREADS<W>) void rmsnorm_grad_kernel(NormGradArgs a)
 {

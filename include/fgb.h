@@ -796,8 +796,8 @@ size_t grad_sumsq_workspace_size(const int64_t *numel, int n);
  * grad_clip -- the global norm of n gradients, and their clipping to it.
  *   norm = scale * sqrt(sum of squares), out = grad * scale * min(1, max_norm / norm), the
  *   factor in FP32 (in FP64 where it is not in that range), the product rounded to FP32, then
- *   to the output's type (BF16: nearest even).  A norm that is infinite or NaN in FP32 clips nothing (out = grad * scale); the
- *   caller sees it in `norm`.
+ *   to the output's type (BF16: nearest even).  A norm that is infinite or NaN in FP32 clips
+ *   nothing (out = grad * scale); the caller sees it in `norm`.
  *   grads, numel, dtypes : as for grad_sumsq; outs, out_dtypes: where the clipped gradients
  *               go, each in its own type.  An output may be its gradient itself (of the same
  *               type), and may lie over nothing else of the list
